@@ -341,6 +341,150 @@ moe_status_t moe_unpermute(const void* y, const int32_t* flat_to_row, const floa
                            int T, int K, int H, const void* shared_y,
                            const float* shared_gate, void* out, moe_stream_t stream);
 
+/* element type of a norm weight */
+#define MOE_DT_BF16 0
+#define MOE_DT_F32 1
+
+/*
+ * N: root-mean-square norm with the residual's addition, ahead of the layer.
+ *   h[t]  = x[t] + residual[t]                        (fp32)
+ *   s[t]  = 1 / sqrt(mean_j h[t,j]^2 + eps)
+ *   y[t]  = h[t] * s[t] * weight
+ * and, where yq is given, y once more in 8 bits, as FP8 expert GEMMs read it:
+ * per column group scale = max |y| / 448 (IEEE fp32 division, 0 for an all-zero
+ * group), code = e4m3(y / scale) rounded to nearest even, saturated at 448.
+ * y is rounded to bf16 and to e4m3 from the fp32 value each; the norm is that
+ * of the unrounded h.
+ *   x         [T, H] bf16;  residual [T, H] bf16 or NULL
+ *   weight    [H] bf16 or fp32 (weight_dtype MOE_DT_BF16 / MOE_DT_F32)
+ *   eps       > 0, finite
+ *   h         [T, H] bf16 output (the new residual stream) or NULL; without a
+ *             residual h is x and must be NULL
+ *   y         [T, H] bf16 output or NULL (not both y and yq NULL)
+ *   rstd      [T] fp32 output s, or NULL (the backward pass needs it)
+ *   yq        [T, H] e4m3 output or NULL, with
+ *   yq_scale  [T, ceil(H / 128)] fp32 (q_group 128, the last group may be
+ *             narrower: the W8A8 activation format) or [T] (q_group 0: one
+ *             scale per row)
+ * h may be x or residual themselves, y may be x (when h is not); the outputs
+ * otherwise overlap nothing.  H % 16 == 0, H <= 32768 (else
+ * MOE_ERR_UNSUPPORTED); pointers of bf16, e4m3 and the weight 16-byte aligned.
+ * A row of h holding a NaN or an infinity gives NaN codes and scales.
+ */
+moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* weight,
+                             int weight_dtype, int T, int H, float eps, void* h, void* y,
+                             float* rstd, void* yq, float* yq_scale, int q_group,
+                             moe_stream_t stream);
+
+/* Scratch bytes moe_add_rmsnorm_backward needs for (T, H). */
+moe_status_t moe_add_rmsnorm_backward_scratch_bytes(int T, int H, size_t* bytes);
+
+/*
+ * Gradient of moe_add_rmsnorm's y.  With n[t] = h[t] * rstd[t]:
+ *   dx[t]   = rstd[t] * (dy[t] * weight - n[t] * mean_j(dy[t] * weight * n[t])) + dh[t]
+ *   dweight = sum_t dy[t] * n[t]
+ * dx is the gradient of x and of residual alike.
+ *   dy [T, H] bf16;  dh [T, H] bf16 or NULL (the gradient that reaches h along
+ *   the residual stream);  h [T, H] bf16 as the forward pass stored it (x where
+ *   there was no residual);  rstd [T] fp32 as the forward pass stored it
+ *   dx [T, H] bf16 output, may be dy or dh;  dweight [H] fp32 output
+ *   scratch  >= moe_add_rmsnorm_backward_scratch_bytes(T, H), 256-byte aligned
+ * Deterministic: the rows' sum has a fixed order for given (T, H).  T == 0
+ * writes dweight = 0.  Sizes and alignment as moe_add_rmsnorm.
+ */
+moe_status_t moe_add_rmsnorm_backward(const void* dy, const void* dh, const void* h,
+                                      const float* rstd, const void* weight, int weight_dtype,
+                                      int T, int H, void* dx, float* dweight, void* scratch,
+                                      size_t scratch_bytes, moe_stream_t stream);
+
+/* Scratch bytes moe_balance_loss needs. */
+moe_status_t moe_balance_loss_scratch_bytes(int T, int E, int n_seq, size_t* bytes);
+
+/*
+ * L: per-expert counts, load-balance loss and router z-loss of a routed batch.
+ * The T tokens are n_seq sequences of T / n_seq each; token_mask leaves tokens
+ * (padding) out.  With n[s] the kept tokens of sequence s, S+ the number of
+ * sequences that keep any and N their sum:
+ *   p[t, e]         = softmax(logits[t, 0..E))[e]           (mode 0), or
+ *                     sigmoid(logits[t, e]) / sum_i sigmoid(logits[t, i]) (mode 1)
+ *   counts[s, e]    = replicas of kept tokens of s with id e
+ *   mean_prob[s, e] = sum_t p[t, e] / n[s]                  (0 where n[s] is 0)
+ *   losses[0]       = 1/S+ sum_s sum_e (E counts[s, e] / (K n[s])) mean_prob[s, e]
+ *   losses[1]       = 1/N sum_t (log sum_e exp logits[t, e])^2
+ *   valid           = n[0], ..., n[n_seq - 1], N, S+
+ * Both losses are 0 where nothing is kept.  A kept row whose E logits are all
+ * -inf counts as a token with p = 0 and log-sum-exp 0; a NaN in a kept row
+ * reaches the losses and its sequence's mean_prob; rows that the mask leaves
+ * out may hold anything.
+ *   logits     [T, ld_logits] fp32, ld_logits >= E (columns from E on, such as
+ *              the shared gate's, are not read)
+ *   ids        [T, K] int32; an id outside [0, E) is not counted and sets
+ *              MOE_DEV_BAD_EXPERT_ID (ids of masked tokens are not read)
+ *   token_mask [T] uint8, 0 = left out, or NULL = all kept
+ *   counts [n_seq, E] int32, mean_prob [n_seq, E] fp32, valid [n_seq + 2]
+ *   int32, losses [2] fp32: outputs
+ *   scratch    >= moe_balance_loss_scratch_bytes(T, E, n_seq), 256-byte
+ *              aligned, zero before the first call; every call leaves it zero
+ *              again, so calls of other sizes may share it (in stream order)
+ * T % n_seq == 0.  T == 0 writes zeros.  Deterministic: sums over blocks are
+ * integers.
+ */
+moe_status_t moe_balance_loss(const float* logits, int ld_logits, const int32_t* ids,
+                              const uint8_t* token_mask, int T, int E, int K, int n_seq, int mode,
+                              int32_t* counts, float* mean_prob, int32_t* valid, float* losses,
+                              void* scratch, size_t scratch_bytes, int32_t* dev_status,
+                              moe_stream_t stream);
+
+/*
+ * Gradient with respect to the router's logits, in one pass: of the routing
+ * weights (d_weights), of the shared expert's gate (d_shared_gate) and of
+ * moe_balance_loss's two losses (grad_losses).  The counts carry no gradient.
+ * For a kept token t of sequence s, a[e] = grad_losses[0] E counts[s, e] /
+ * (K n[s]^2 S+):
+ *   dlogits[t, e]  = p[t, e] (a[e] - sum_i a[i] p[t, i])  (* (1 - sigmoid) in mode 1)
+ *                  + 2 grad_losses[1] lse[t] softmax(logits[t])[e] / N
+ *   dlogits[t, ids[t, k]] += weights[t, k] (d_weights[t, k]
+ *                    - sum_j weights[t, j] d_weights[t, j] / scale) (* (1 - sigmoid) in mode 1)
+ *   dlogits[t, E]  = d_shared_gate[t] g (1 - g), g = sigmoid(logits[t, E])
+ * with scale 1 in mode 0.  Rows of tokens that the mask leaves out are zero.
+ *   logits [T, ld_logits];  dlogits [T, ld_dlogits] output, not logits itself;
+ *   columns from E on (E + 1 on with d_shared_gate) are not written
+ *   ids, weights [T, K] as moe_topk_route gave them (same mode and scale); an
+ *   id outside [0, E) adds nothing and sets MOE_DEV_BAD_EXPERT_ID
+ *   d_weights [T, K] fp32 or NULL;  d_shared_gate [T] fp32 or NULL (needs
+ *   ld_logits and ld_dlogits >= E + 1)
+ *   counts, valid as moe_balance_loss gave them (same mask and n_seq) and
+ *   grad_losses [2] fp32 (device), or grad_losses NULL: no losses
+ */
+moe_status_t moe_route_backward(const float* logits, int ld_logits, const int32_t* ids,
+                                const float* weights, const float* d_weights,
+                                const float* d_shared_gate, const uint8_t* token_mask, int T,
+                                int E, int K, int n_seq, int mode, float scale,
+                                const int32_t* counts, const int32_t* valid,
+                                const float* grad_losses, float* dlogits, int ld_dlogits,
+                                int32_t* dev_status, moe_stream_t stream);
+
+/*
+ * Gradient of moe_unpermute:
+ *   dy[row]          = weights[t, k] * dout[t],      row = flat_to_row[t*K + k]
+ *   d_weights[t, k]  = <dout[t], y[row]>             (0 for a dropped replica)
+ *   d_shared_y[t]    = shared_gate[t] * dout[t]
+ *   d_shared_gate[t] = <dout[t], shared_y[t]>
+ * Each output may be NULL (not all of them); y is read for d_weights, weights
+ * for dy, shared_y for d_shared_gate and shared_gate for d_shared_y, and may be
+ * NULL without them.  Rows of dy that no replica maps to are left untouched; a
+ * flat_to_row outside [0, T*K) is a dropped replica.
+ *   dout [T, H] bf16;  y, dy [T*K, H] bf16;  shared_y, d_shared_y [T, H] bf16;
+ *   weights, d_weights [T, K] fp32;  shared_gate, d_shared_gate [T] fp32
+ * dy may be y, d_shared_y may be shared_y.  H % 8 == 0, H <= 32768 (else
+ * MOE_ERR_UNSUPPORTED).  Deterministic.
+ */
+moe_status_t moe_unpermute_backward(const void* dout, const void* y, const int32_t* flat_to_row,
+                                    const float* weights, int T, int K, int H,
+                                    const void* shared_y, const float* shared_gate, void* dy,
+                                    float* d_weights, void* d_shared_y, float* d_shared_gate,
+                                    moe_stream_t stream);
+
 /* Workspace bytes moe_layer needs for cfg (sized for cfg->T_max). */
 moe_status_t moe_workspace_bytes(const moe_config_t* cfg, size_t* bytes);
 

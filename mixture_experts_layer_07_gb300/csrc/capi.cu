@@ -47,6 +47,21 @@ moe_status_t check_cfg(const moe_config_t* c) {
   return MOE_OK;
 }
 
+moe_status_t check_norm(int T, int H, int weight_dtype) {
+  if (T < 0 || H <= 0 || H % 16 != 0) return MOE_ERR_INVALID_ARG;
+  if (weight_dtype != MOE_DT_BF16 && weight_dtype != MOE_DT_F32) return MOE_ERR_INVALID_ARG;
+  return H > kRowMaxH ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// a routed batch of n_seq sequences of T / n_seq tokens
+moe_status_t check_router(int T, int E, int K, int n_seq, int mode) {
+  if (T < 0 || E <= 0 || E > 1024 || K <= 0 || K > E || K > 32) return MOE_ERR_INVALID_ARG;
+  if (n_seq <= 0 || T % n_seq != 0 || (int64_t)T * K > 0x7fffffff) return MOE_ERR_INVALID_ARG;
+  if (mode != MOE_SCORE_SOFTMAX_RENORM && mode != MOE_SCORE_SIGMOID_BIAS_SCALED)
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
 // byte offset of the one-launch small-batch layer's counters inside `sync`
 // (after the fused routing's 256 bytes and the K-slice counters)
 size_t decode_sync_offset(const moe_config_t* c) {
@@ -282,6 +297,134 @@ moe_status_t moe_unpermute(const void* y, const int32_t* flat_to_row, const floa
     return MOE_ERR_MISALIGNED;
   return cuda_status(
       launch_unpermute(y, flat_to_row, weights, T, K, H, shared_y, shared_gate, out, stream));
+}
+
+moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* weight,
+                             int weight_dtype, int T, int H, float eps, void* h, void* y,
+                             float* rstd, void* yq, float* yq_scale, int q_group,
+                             moe_stream_t stream) {
+  const moe_status_t s = check_norm(T, H, weight_dtype);
+  if (s != MOE_OK) return s;
+  if (!(eps > 0.f) || !(eps < 3.4e38f)) return MOE_ERR_INVALID_ARG;
+  if ((h && !residual) || (!y && !yq) || (yq == nullptr) != (yq_scale == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (yq && q_group != 0 && q_group != 128) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !weight) return MOE_ERR_INVALID_ARG;
+  if (y && (y == h || y == residual)) return MOE_ERR_INVALID_ARG;
+  if (misaligned(x, 16) || misaligned(residual, 16) || misaligned(weight, 16) ||
+      misaligned(h, 16) || misaligned(y, 16) || misaligned(yq, 16) || misaligned(rstd, 4) ||
+      misaligned(yq_scale, 4))
+    return MOE_ERR_MISALIGNED;
+  return cuda_status(launch_add_rmsnorm(x, residual, weight, weight_dtype == MOE_DT_F32, T, H, eps,
+                                        h, y, rstd, yq, yq_scale, q_group, stream));
+}
+
+moe_status_t moe_add_rmsnorm_backward_scratch_bytes(int T, int H, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const moe_status_t s = check_norm(T, H, MOE_DT_BF16);
+  if (s != MOE_OK) return s;
+  *bytes = add_rmsnorm_backward_scratch_bytes(T, H);
+  return MOE_OK;
+}
+
+moe_status_t moe_add_rmsnorm_backward(const void* dy, const void* dh, const void* h,
+                                      const float* rstd, const void* weight, int weight_dtype,
+                                      int T, int H, void* dx, float* dweight, void* scratch,
+                                      size_t scratch_bytes, moe_stream_t stream) {
+  const moe_status_t s = check_norm(T, H, weight_dtype);
+  if (s != MOE_OK) return s;
+  if (!dweight || !scratch) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!dy || !h || !rstd || !weight || !dx)) return MOE_ERR_INVALID_ARG;
+  if (scratch_bytes < add_rmsnorm_backward_scratch_bytes(T, H)) return MOE_ERR_WORKSPACE;
+  if (misaligned(dy, 16) || misaligned(dh, 16) || misaligned(h, 16) || misaligned(weight, 16) ||
+      misaligned(dx, 16) || misaligned(rstd, 4) || misaligned(dweight, 4) ||
+      misaligned(scratch, 256))
+    return MOE_ERR_MISALIGNED;
+  return cuda_status(launch_add_rmsnorm_backward(dy, dh, h, rstd, weight,
+                                                 weight_dtype == MOE_DT_F32, T, H, dx, dweight,
+                                                 scratch, stream));
+}
+
+moe_status_t moe_balance_loss_scratch_bytes(int T, int E, int n_seq, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const moe_status_t s = check_router(T, E, 1, n_seq, MOE_SCORE_SOFTMAX_RENORM);
+  if (s != MOE_OK) return s;
+  *bytes = balance_loss_scratch_bytes(T, E, n_seq);
+  return MOE_OK;
+}
+
+moe_status_t moe_balance_loss(const float* logits, int ld_logits, const int32_t* ids,
+                              const uint8_t* token_mask, int T, int E, int K, int n_seq, int mode,
+                              int32_t* counts, float* mean_prob, int32_t* valid, float* losses,
+                              void* scratch, size_t scratch_bytes, int32_t* dev_status,
+                              moe_stream_t stream) {
+  const moe_status_t s = check_router(T, E, K, n_seq, mode);
+  if (s != MOE_OK) return s;
+  if (ld_logits < E) return MOE_ERR_INVALID_ARG;
+  if (!counts || !mean_prob || !valid || !losses || !scratch) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !ids)) return MOE_ERR_INVALID_ARG;
+  if (scratch_bytes < balance_loss_scratch_bytes(T, E, n_seq)) return MOE_ERR_WORKSPACE;
+  if (misaligned(logits, 4) || misaligned(ids, 4) || misaligned(counts, 4) ||
+      misaligned(mean_prob, 4) || misaligned(valid, 4) || misaligned(losses, 4) ||
+      misaligned(scratch, 256) || misaligned(dev_status, 4))
+    return MOE_ERR_MISALIGNED;
+  return cuda_status(launch_balance_loss(logits, ld_logits, ids, token_mask, T, E, K, n_seq, mode,
+                                         counts, mean_prob, valid, losses, scratch, dev_status,
+                                         stream));
+}
+
+moe_status_t moe_route_backward(const float* logits, int ld_logits, const int32_t* ids,
+                                const float* weights, const float* d_weights,
+                                const float* d_shared_gate, const uint8_t* token_mask, int T,
+                                int E, int K, int n_seq, int mode, float scale,
+                                const int32_t* counts, const int32_t* valid,
+                                const float* grad_losses, float* dlogits, int ld_dlogits,
+                                int32_t* dev_status, moe_stream_t stream) {
+  const moe_status_t s = check_router(T, E, K, n_seq, mode);
+  if (s != MOE_OK) return s;
+  const int cols = E + (d_shared_gate ? 1 : 0);
+  if (ld_logits < cols || ld_dlogits < cols) return MOE_ERR_INVALID_ARG;
+  if (d_weights && (!weights || !ids)) return MOE_ERR_INVALID_ARG;
+  if (grad_losses && (!counts || !valid)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!logits || !dlogits || logits == dlogits) return MOE_ERR_INVALID_ARG;
+  if (misaligned(logits, 4) || misaligned(ids, 4) || misaligned(weights, 4) ||
+      misaligned(d_weights, 4) || misaligned(d_shared_gate, 4) || misaligned(counts, 4) ||
+      misaligned(valid, 4) || misaligned(grad_losses, 4) || misaligned(dlogits, 4) ||
+      misaligned(dev_status, 4))
+    return MOE_ERR_MISALIGNED;
+  RouteBackwardArgs a;
+  a.logits = logits; a.ids = ids; a.weights = weights; a.d_weights = d_weights;
+  a.d_shared_gate = d_shared_gate; a.mask = token_mask; a.counts = counts; a.valid = valid;
+  a.grad_losses = grad_losses; a.dlogits = dlogits; a.dev_status = dev_status;
+  a.ld = ld_logits; a.ld_d = ld_dlogits; a.T = T; a.E = E; a.K = K; a.n_seq = n_seq;
+  a.mode = mode; a.scale = scale;
+  return cuda_status(launch_route_backward(a, stream));
+}
+
+moe_status_t moe_unpermute_backward(const void* dout, const void* y, const int32_t* flat_to_row,
+                                    const float* weights, int T, int K, int H,
+                                    const void* shared_y, const float* shared_gate, void* dy,
+                                    float* d_weights, void* d_shared_y, float* d_shared_gate,
+                                    moe_stream_t stream) {
+  if (T < 0 || K <= 0 || H <= 0 || H % 8 != 0) return MOE_ERR_INVALID_ARG;
+  if ((int64_t)T * K > 0x7fffffff) return MOE_ERR_INVALID_ARG;
+  if (H > kRowMaxH) return MOE_ERR_UNSUPPORTED;
+  if (!dy && !d_weights && !d_shared_y && !d_shared_gate) return MOE_ERR_INVALID_ARG;
+  if ((d_weights && !y) || (dy && !weights) || (d_shared_gate && !shared_y) ||
+      (d_shared_y && !shared_gate))
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!dout || ((dy || d_weights) && !flat_to_row)) return MOE_ERR_INVALID_ARG;
+  if (misaligned(dout, 16) || misaligned(y, 16) || misaligned(dy, 16) ||
+      misaligned(shared_y, 16) || misaligned(d_shared_y, 16) || misaligned(flat_to_row, 4) ||
+      misaligned(weights, 4) || misaligned(d_weights, 4) || misaligned(shared_gate, 4) ||
+      misaligned(d_shared_gate, 4))
+    return MOE_ERR_MISALIGNED;
+  return cuda_status(launch_unpermute_backward(dout, y, flat_to_row, weights, T, K, H, shared_y,
+                                               shared_gate, dy, d_weights, d_shared_y,
+                                               d_shared_gate, stream));
 }
 
 moe_status_t moe_workspace_layout(const moe_config_t* cfg, moe_workspace_layout_t* layout) {

@@ -166,6 +166,47 @@ cudaError_t launch_unpermute(const void* y, const int32_t* flat_to_row, const fl
                              int T, int K, int H, const void* shared_y, const float* shared_gate,
                              void* out, cudaStream_t stream);
 
+// RMS norm with the residual's addition (norm.cu); q_group 128 or 0 (one scale
+// per row) where yq is given.
+constexpr int kRowMaxH = 32768;  // widest row of norm.cu and unpermute_grad.cu
+cudaError_t launch_add_rmsnorm(const void* x, const void* residual, const void* w, bool w32, int T,
+                               int H, float eps, void* h, void* y, float* rstd, void* yq,
+                               float* yscale, int q_group, cudaStream_t stream);
+size_t add_rmsnorm_backward_scratch_bytes(int T, int H);
+cudaError_t launch_add_rmsnorm_backward(const void* dy, const void* dh, const void* h,
+                                        const float* rstd, const void* w, bool w32, int T, int H,
+                                        void* dx, float* dweight, void* scratch,
+                                        cudaStream_t stream);
+
+// Router losses and gradient (route_grad.cu).  The losses' scratch must be
+// zero before the first call and is zero again after each.
+size_t balance_loss_scratch_bytes(int T, int E, int n_seq);
+cudaError_t launch_balance_loss(const float* logits, int ld, const int32_t* ids,
+                                const uint8_t* mask, int T, int E, int K, int n_seq, int mode,
+                                int32_t* counts, float* mean_prob, int32_t* valid, float* losses,
+                                void* scratch, int32_t* dev_status, cudaStream_t stream);
+struct RouteBackwardArgs {
+  const float* logits;
+  const int32_t* ids;
+  const float *weights, *d_weights;  // d_weights nullable
+  const float* d_shared_gate;        // nullable
+  const uint8_t* mask;               // nullable
+  const int32_t *counts, *valid;     // with grad_losses
+  const float* grad_losses;          // nullable: no losses
+  float* dlogits;
+  int32_t* dev_status;
+  int ld, ld_d, T, E, K, n_seq, mode;
+  float scale;
+};
+cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t stream);
+
+// Gradient of the weighted unpermute (unpermute_grad.cu).
+cudaError_t launch_unpermute_backward(const void* dout, const void* y, const int32_t* flat_to_row,
+                                      const float* weights, int T, int K, int H,
+                                      const void* shared_y, const float* shared_gate, void* dy,
+                                      float* d_weights, void* d_shared_y, float* d_shared_gate,
+                                      cudaStream_t stream);
+
 // The whole layer for small batches in one cooperative launch (decode_layer.cu):
 // router, top-K, permute, G1/G2 (+ shared expert) and combine.  The sync
 // words must be zero before the launch and are zero again after it.

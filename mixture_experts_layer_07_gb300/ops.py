@@ -33,9 +33,13 @@ EXPORTS = ["moe_status_string", "moe_default_m_skinny", "moe_block_variant", "mo
            "moe_grouped_gemm_scratch_bytes", "moe_grouped_gemm_scratch_bytes_ex",
            "moe_grouped_gemm", "moe_unpermute",
            "moe_workspace_bytes", "moe_layer", "moe_workspace_layout", "moe_permute_static",
-           "moe_router_tc_scratch_bytes", "moe_router_gemm_tc", "moe_bounded_wait_check"]
+           "moe_router_tc_scratch_bytes", "moe_router_gemm_tc", "moe_bounded_wait_check",
+           "moe_add_rmsnorm", "moe_add_rmsnorm_backward_scratch_bytes",
+           "moe_add_rmsnorm_backward", "moe_balance_loss_scratch_bytes", "moe_balance_loss",
+           "moe_route_backward", "moe_unpermute_backward"]
 
 PERMUTE_STATIC_SCRATCH_BYTES = 1 << 20
+DT_BF16, DT_F32 = 0, 1
 
 
 class MoEError(RuntimeError):
@@ -102,6 +106,15 @@ def _lib():
             "moe_layer": [ctypes.POINTER(Config), _I, _P, ctypes.POINTER(Weights), _P, _P, _S,
                           _P, _P],
             "moe_bounded_wait_check": [_P, _I, _I, _P, _P],
+            "moe_add_rmsnorm": [_P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _P, _P, _I, _P],
+            "moe_add_rmsnorm_backward_scratch_bytes": [_I, _I, ctypes.POINTER(_S)],
+            "moe_add_rmsnorm_backward": [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _S, _P],
+            "moe_balance_loss_scratch_bytes": [_I, _I, _I, ctypes.POINTER(_S)],
+            "moe_balance_loss": [_P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _S, _P,
+                                 _P],
+            "moe_route_backward": [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P,
+                                   _P, _I, _P, _P],
+            "moe_unpermute_backward": [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -255,6 +268,113 @@ def unpermute(y, flat_to_row, weights, T, K, H, out, shared_y=None, shared_gate=
               stream=None):
     _check(_lib().moe_unpermute(_p(y), _p(flat_to_row), _p(weights), T, K, H, _p(shared_y),
                                 _p(shared_gate), _p(out), _stream(stream)), "moe_unpermute")
+
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_MASK = (torch.uint8, torch.bool)
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)  # codes, as either
+
+
+def _pc(t, dtype, numel, name):
+    """Device pointer of a tensor (or None) that must hold `numel` values of `dtype`."""
+    if t is None:
+        return None
+    if (t.dtype not in dtype) if isinstance(dtype, tuple) else (t.dtype != dtype):
+        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor of {numel} values expected, got shape "
+                         f"{tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _norm_weight(weight, H):
+    f32 = weight.dtype == _F32
+    return _pc(weight, _F32 if f32 else _BF16, H, "weight"), DT_F32 if f32 else DT_BF16
+
+
+def add_rmsnorm(x, weight, eps, y, *, residual=None, h=None, rstd=None, yq=None, yq_scale=None,
+                q_group=128, stream=None):
+    """y = rmsnorm(x + residual) * weight, h = x + residual; yq / yq_scale: y as e4m3 codes with
+    a scale per 128 columns (q_group 128) or per row (q_group 0)."""
+    T, H = x.shape
+    w, wdt = _norm_weight(weight, H)
+    n = T * H
+    _check(_lib().moe_add_rmsnorm(
+        _pc(x, _BF16, n, "x"), _pc(residual, _BF16, n, "residual"), w, wdt, T, H, eps,
+        _pc(h, _BF16, n, "h"), _pc(y, _BF16, n, "y"), _pc(rstd, _F32, T, "rstd"),
+        _pc(yq, _E4M3, n, "yq"),
+        _pc(yq_scale, _F32, T * (-(-H // 128) if q_group else 1), "yq_scale"), q_group,
+        _stream(stream)), "moe_add_rmsnorm")
+
+
+def add_rmsnorm_backward_scratch_bytes(T: int, H: int) -> int:
+    n = _S()
+    _check(_lib().moe_add_rmsnorm_backward_scratch_bytes(T, H, ctypes.byref(n)),
+           "moe_add_rmsnorm_backward_scratch_bytes")
+    return n.value
+
+
+def add_rmsnorm_backward(dy, h, rstd, weight, dx, dweight, scratch, *, dh=None, stream=None):
+    T, H = h.shape
+    w, wdt = _norm_weight(weight, H)
+    n = T * H
+    _check(_lib().moe_add_rmsnorm_backward(
+        _pc(dy, _BF16, n, "dy"), _pc(dh, _BF16, n, "dh"), _pc(h, _BF16, n, "h"),
+        _pc(rstd, _F32, T, "rstd"), w, wdt, T, H, _pc(dx, _BF16, n, "dx"),
+        _pc(dweight, _F32, H, "dweight"), _p(scratch), scratch.numel() * scratch.element_size(),
+        _stream(stream)), "moe_add_rmsnorm_backward")
+
+
+def balance_loss_scratch_bytes(T: int, E: int, n_seq: int = 1) -> int:
+    n = _S()
+    _check(_lib().moe_balance_loss_scratch_bytes(T, E, n_seq, ctypes.byref(n)),
+           "moe_balance_loss_scratch_bytes")
+    return n.value
+
+
+def balance_loss(logits, ids, E, counts, mean_prob, valid, losses, scratch, *, n_seq=1,
+                 mode=MODE_SOFTMAX, token_mask=None, dev_status=None, stream=None):
+    """counts, mean_prob [n_seq, E], valid [n_seq + 2] and losses [2] (load balance, router z) of
+    a routed batch; see the header."""
+    T, ld = logits.shape
+    K = ids.shape[1]
+    _check(_lib().moe_balance_loss(
+        _pc(logits, _F32, T * ld, "logits"), ld, _pc(ids, _I32, T * K, "ids"),
+        _pc(token_mask, _MASK, T, "token_mask"), T, E, K, n_seq, mode,
+        _pc(counts, _I32, n_seq * E, "counts"), _pc(mean_prob, _F32, n_seq * E, "mean_prob"),
+        _pc(valid, _I32, n_seq + 2, "valid"), _pc(losses, _F32, 2, "losses"), _p(scratch),
+        scratch.numel() * scratch.element_size(), _p(dev_status), _stream(stream)),
+        "moe_balance_loss")
+
+
+def route_backward(logits, ids, E, dlogits, *, mode=MODE_SOFTMAX, scale=1.0, weights=None,
+                   d_weights=None, d_shared_gate=None, token_mask=None, n_seq=1, counts=None,
+                   valid=None, grad_losses=None, dev_status=None, stream=None):
+    """dlogits from the gradients of the routing weights, the shared gate and balance_loss's two
+    losses; see the header."""
+    T, ld = logits.shape
+    K, ldd = ids.shape[1], dlogits.shape[1]
+    _check(_lib().moe_route_backward(
+        _pc(logits, _F32, T * ld, "logits"), ld, _pc(ids, _I32, T * K, "ids"),
+        _pc(weights, _F32, T * K, "weights"), _pc(d_weights, _F32, T * K, "d_weights"),
+        _pc(d_shared_gate, _F32, T, "d_shared_gate"), _pc(token_mask, _MASK, T, "token_mask"), T,
+        E, K, n_seq, mode, scale, _pc(counts, _I32, n_seq * E, "counts"),
+        _pc(valid, _I32, n_seq + 2, "valid"), _pc(grad_losses, _F32, 2, "grad_losses"),
+        _pc(dlogits, _F32, T * ldd, "dlogits"), ldd, _p(dev_status), _stream(stream)),
+        "moe_route_backward")
+
+
+def unpermute_backward(dout, flat_to_row, weights, T, K, H, *, y=None, dy=None, d_weights=None,
+                       shared_y=None, shared_gate=None, d_shared_y=None, d_shared_gate=None,
+                       stream=None):
+    n, r = T * H, T * K * H
+    _check(_lib().moe_unpermute_backward(
+        _pc(dout, _BF16, n, "dout"), _pc(y, _BF16, r, "y"),
+        _pc(flat_to_row, _I32, T * K, "flat_to_row"), _pc(weights, _F32, T * K, "weights"), T, K,
+        H, _pc(shared_y, _BF16, n, "shared_y"), _pc(shared_gate, _F32, T, "shared_gate"),
+        _pc(dy, _BF16, r, "dy"), _pc(d_weights, _F32, T * K, "d_weights"),
+        _pc(d_shared_y, _BF16, n, "d_shared_y"), _pc(d_shared_gate, _F32, T, "d_shared_gate"),
+        _stream(stream)), "moe_unpermute_backward")
 
 
 def layer(cfg: Config, x, weights: Weights, out, workspace, dev_status=None, stream=None, T=None):
