@@ -140,8 +140,8 @@ def _p(t):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # torch.cuda.current_stream().cuda_stream without its Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -279,7 +279,7 @@ def _pc(t, dtype, numel, name):
     """Device pointer of a tensor (or None) that must hold `numel` values of `dtype`."""
     if t is None:
         return None
-    if (t.dtype not in dtype) if isinstance(dtype, tuple) else (t.dtype != dtype):
+    if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
         raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
     if t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous tensor of {numel} values expected, got shape "
