@@ -4,7 +4,7 @@
 //   dy[row(t,k)] = w[t,k] * d        dw[t,k] = <d, y[row(t,k)]>
 //   dsh[t]       = g[t] * d          dg[t]   = <d, sh[t]>
 // One pass: a block holds d in registers (VPT 16-byte vectors per thread) and
-// walks the token's rows in groups of up to KB, each row read and its gradient
+// walks the token's rows in groups of KB, each row read and its gradient
 // written once; the dot products of a group are reduced together.  Bound by
 // memory.  No atomics: every row belongs to one (t, k).
 #include "common.cuh"
@@ -13,7 +13,6 @@
 namespace {
 
 constexpr int kMaxWarps = 16;
-constexpr int KB = 4;  // rows in flight
 
 MOE_DEVICE float dot8(const uint4& v, const float* d, float s) {
   float f[8];
@@ -30,7 +29,7 @@ MOE_DEVICE uint4 scaled8(const float* d, float w) {
 
 // Row index K of the walk stands for the shared expert's row.  y and dy (and
 // the shared pair) are not __restrict__: they may be the same buffer.
-template <int VPT, int MAXT>
+template <int VPT, int KB, int MAXT>
 __global__ void __launch_bounds__(MAXT)
 unpermute_backward_kernel(const uint4* __restrict__ dout, const uint4* y,
                           const int32_t* __restrict__ flat_to_row,
@@ -73,17 +72,26 @@ unpermute_backward_kernel(const uint4* __restrict__ dout, const uint4* y,
       }
       acc[i] = 0.f;
     }
+    // every vector of the group in flight before the first one is used
+    uint4 v[KB][VPT];
 #pragma unroll
     for (int i = 0; i < KB; ++i) {
       const uint4* src = shared[i] ? shared_y : y;
-      uint4* dst = shared[i] ? d_shared_y : dy;
-      if (row[i] < 0) continue;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         const int c = threadIdx.x + blockDim.x * j;
-        if (c >= H8) continue;
-        if (src) acc[i] = dot8(src[(size_t)row[i] * H8 + c], d[j], acc[i]);
-        if (dst) dst[(size_t)row[i] * H8 + c] = scaled8(d[j], wk[i]);
+        v[i][j] = src && row[i] >= 0 && c < H8 ? src[(size_t)row[i] * H8 + c]
+                                               : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {
+      uint4* dst = shared[i] ? d_shared_y : dy;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int c = threadIdx.x + blockDim.x * j;
+        acc[i] = dot8(v[i][j], d[j], acc[i]);
+        if (dst && row[i] >= 0 && c < H8) dst[(size_t)row[i] * H8 + c] = scaled8(d[j], wk[i]);
       }
     }
 #pragma unroll
@@ -116,10 +124,10 @@ cudaError_t launch_unpermute_backward(const void* dout, const void* y, const int
   const int H8 = H / 8;
   const int vpt = H8 <= 64 ? 1 : H8 <= 128 ? 2 : H8 <= 1024 ? 4 : 8;
   const int threads = moe_cdiv(H8, 32 * vpt) * 32;
-  auto k = vpt == 1   ? unpermute_backward_kernel<1, 256>
-           : vpt == 2 ? unpermute_backward_kernel<2, 256>
-           : vpt == 4 ? unpermute_backward_kernel<4, 256>
-                      : unpermute_backward_kernel<8, 512>;
+  auto k = vpt == 1   ? unpermute_backward_kernel<1, 4, 256>
+           : vpt == 2 ? unpermute_backward_kernel<2, 4, 256>
+           : vpt == 4 ? unpermute_backward_kernel<4, 4, 256>
+                      : unpermute_backward_kernel<8, 2, 512>;
   // inputs that no requested output needs are not read
   return moe_launch(k, dim3(T), dim3(threads), 0, stream, 1, static_cast<const uint4*>(dout),
                     static_cast<const uint4*>(d_weights ? y : nullptr),
