@@ -56,90 +56,130 @@ MOE_DEVICE float group_max(float v) {
   return v;
 }
 
-// What a row's logits turn into (-inf past E): its probabilities, log-sum-exp
-// (0 for a row of -inf) and sum of exponentials relative to the maximum.
-template <int NPL>
-struct Row {
-  float p[NPL];
-  float lse, sum;
-};
-
-// sigmoid(l) * exp(c), c = max(0, -row maximum): the common factor cancels in
-// p and keeps rows of very negative logits from vanishing
-MOE_DEVICE float scaled_sigmoid(float l, float c) {
-  const float a = __expf(-fabsf(l));
-  return (l > 0.f ? 1.f : expf(l + c)) / (1.f + a);  // l > 0 makes c 0
+// e^x as one hardware 2^x: x is at most 0 wherever this is used, or cancels in
+// a ratio; its relative error is about |x| 2^-24 + 2^-22
+MOE_DEVICE float exp_fast(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+// 1 / x for 1 <= x <= 2
+MOE_DEVICE float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // 1 - sigmoid(l)
 MOE_DEVICE float sigmoid_tail(float l) {
-  const float a = __expf(-fabsf(l));
-  return (l > 0.f ? a : 1.f) / (1.f + a);
+  const float a = exp_fast(-fabsf(l));
+  return (l > 0.f ? a : 1.f) * rcp_fast(1.f + a);
 }
 
+// What a row's logits v turn into (-inf past E): weights u, their probabilities
+// u * inv, the maximum (0 for a row of -inf), log-sum-exp (0 for such a row)
+// and 1 / sum of e^(v - max) (0 for such a row).
+//   mode 0: u = e^(v - max)
+//   mode 1: u = sigmoid(v) e^c, c = max(0, -max): the common factor cancels in
+//           u * inv and keeps rows of very negative logits from vanishing
+struct RowSums {
+  float max, lse, inv, inv_exp;
+};
+
 template <int LPR, int NPL, int MODE>
-MOE_DEVICE void row_probs(const float (&v)[NPL], Row<NPL>& r) {
+MOE_DEVICE RowSums row_probs(const float (&v)[NPL], float (&u)[NPL]) {
   float m = v[0];
 #pragma unroll
   for (int i = 1; i < NPL; ++i) m = fmaxf(m, v[i]);
   m = group_max<LPR>(m);
   if (m == kNegInf) m = 0.f;
+  RowSums r;
+  r.max = m;
   float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    r.p[i] = expf(v[i] - m);
-    s += r.p[i];
-  }
-  s = group_sum<LPR>(s);
-  r.sum = s;
-  r.lse = s == 0.f ? 0.f : m + logf(s);
   if constexpr (MODE == MOE_SCORE_SOFTMAX_RENORM) {
-    const float inv = s == 0.f ? 0.f : 1.f / s;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) r.p[i] *= inv;
-  } else {
-    const float c = fmaxf(0.f, -m);
-    float q = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      r.p[i] = scaled_sigmoid(v[i], c);
-      q += r.p[i];
+      u[i] = exp_fast(v[i] - m);
+      s += u[i];
     }
-    q = group_sum<LPR>(q);
-    const float inv = q == 0.f ? 0.f : 1.f / q;
+    s = group_sum<LPR>(s);
+  } else {
+    float q = 0.f;
+    if (m >= 0.f) {  // c = 0
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) r.p[i] *= inv;
+      for (int i = 0; i < NPL; ++i) {
+        const float a = exp_fast(-fabsf(v[i]));
+        u[i] = (v[i] > 0.f ? 1.f : a) * rcp_fast(1.f + a);
+        s += exp_fast(v[i] - m);
+        q += u[i];
+      }
+    } else {  // every logit is negative
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        const float e = exp_fast(v[i] - m);
+        u[i] = e * rcp_fast(1.f + exp_fast(v[i]));
+        s += e;
+        q += u[i];
+      }
+    }
+    s = group_sum<LPR>(s);
+    q = group_sum<LPR>(q);
+    r.inv = q == 0.f ? 0.f : 1.f / q;
   }
+  r.lse = s == 0.f ? 0.f : m + logf(s);
+  r.inv_exp = s == 0.f ? 0.f : 1.f / s;
+  if constexpr (MODE == MOE_SCORE_SOFTMAX_RENORM) r.inv = r.inv_exp;
+  return r;
 }
 
-template <int LPR, int NPL>
+// FULL: E == LPR * NPL, no column is missing
+template <int LPR, int NPL, bool FULL>
 MOE_DEVICE void load_row(const float* __restrict__ row, int E, int lig, bool on, float (&v)[NPL]) {
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     const int c = lig + LPR * i;
-    v[i] = on && c < E ? __ldg(row + c) : kNegInf;
+    v[i] = on && (FULL || c < E) ? __ldg(row + c) : kNegInf;
   }
 }
 
+template <typename V>
+MOE_DEVICE V block_sum(V v, V* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if (lane_id() == 0) red[warp_id()] = v;
+  __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) v += red[w];
+  return v;
+}
+
+// Blocks per SM that the registers of a row pair (this row and the next one,
+// loaded ahead) allow; the grid is that many per SM.
+constexpr int blocks_per_sm(int npl) { return npl <= 8 ? 4 : npl <= 16 ? 3 : 2; }
+
 // ---------------------------------------------------------------- forward
-// Block b takes chunk b % chunks of sequence b / chunks.
-template <int LPR, int NPL, int MODE>
-__global__ void __launch_bounds__(kThreads)
+// Block b takes chunk b % chunks of sequence b / chunks.  The last block of a
+// sequence to finish turns its sums into outputs, and the last sequence's
+// block the sequences' losses into the batch's.  A sequence of one block, and
+// a batch of one sequence, skip the hand-over through global memory.
+template <int LPR, int NPL, int MODE, bool FULL>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(NPL))
 balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restrict__ ids,
                const uint8_t* __restrict__ mask, int L, int E, int K, int n_seq, int chunks,
                int rows_per_block, int shift, Scratch sc, int32_t* __restrict__ counts,
                float* __restrict__ mean_prob, int32_t* __restrict__ valid,
                float* __restrict__ losses, int32_t* __restrict__ dev_status) {
   constexpr int RPW = 32 / LPR;
+  constexpr int kStep = kWarps * RPW;
   extern __shared__ float smem[];
   float* psm = smem;                                              // [kWarps][E]
   int32_t* hist = reinterpret_cast<int32_t*>(smem + kWarps * E);  // [E]
-  __shared__ float zred[kWarps];
-  __shared__ int nred[kWarps];
+  __shared__ float fred[kWarps];
+  __shared__ double dred[kWarps];
+  __shared__ int ired[kWarps];
   __shared__ int bad, last;
-  __shared__ double dred[2][kWarps];
-  pdl_wait();
-  pdl_trigger();
   const int seq = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
   const int r0 = chunk * rows_per_block;
   const int r1 = min(L, r0 + rows_per_block);
@@ -148,11 +188,21 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
   const int lig = lane % LPR, sub = lane / LPR;
   for (int e = tid; e < E; e += kThreads) hist[e] = 0;
   if (tid == 0) bad = 0;
+  pdl_wait();
+  pdl_trigger();
   __syncthreads();
 
+  // this row, the next one's logits and the one after's mask are in flight
+  const uint8_t* mrow = mask ? mask + t0 : nullptr;
+  auto kept_row = [&](int r) { return r < r1 && (!mrow || __ldg(mrow + r)); };
+  const float* base = logits + t0 * ld;
+  int r = r0 + warp * RPW + sub;
+  bool on = kept_row(r), on1 = kept_row(r + kStep);
+  float v[NPL];
+  load_row<LPR, NPL, FULL>(base + (size_t)r * ld, E, lig, on, v);
+
   for (int i = tid; i < (r1 - r0) * K; i += kThreads) {
-    const size_t t = t0 + r0 + i / K;
-    if (mask && !__ldg(mask + t)) continue;
+    if (mrow && !__ldg(mrow + r0 + i / K)) continue;
     const int id = __ldg(ids + (t0 + r0) * K + i);
     if ((unsigned)id < (unsigned)E) atomicAdd(&hist[id], 1);
     else moe_set_status(dev_status, MOE_DEV_BAD_EXPERT_ID);
@@ -164,23 +214,23 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
   float z = 0.f;
   int kept = 0;
   bool nan = false;
-  for (int rb = r0 + warp * RPW; rb < r1; rb += kWarps * RPW) {
-    const int r = rb + sub;
-    const size_t t = t0 + r;
-    const bool on = r < r1 && (!mask || __ldg(mask + t));
-    float v[NPL];
-    load_row<LPR, NPL>(logits + t * ld, E, lig, on, v);
-    Row<NPL> w;
-    row_probs<LPR, NPL, MODE>(v, w);
-    if (on) {
+  for (int rb = r0 + warp * RPW; rb < r1; rb += kStep) {
+    float nx[NPL], u[NPL];
+    load_row<LPR, NPL, FULL>(base + (size_t)(r + kStep) * ld, E, lig, on1, nx);
+    const bool on2 = kept_row(r + 2 * kStep);
+    const RowSums w = row_probs<LPR, NPL, MODE>(v, u);  // a row left out gives zeros
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) acc[i] += w.p[i];
-      if (lig == 0) {
-        z = fmaf(w.lse, w.lse, z);
-        ++kept;
-      }
-      nan |= !(w.p[0] == w.p[0]);
+    for (int i = 0; i < NPL; ++i) acc[i] = fmaf(u[i], w.inv, acc[i]);
+    if (on && lig == 0) {
+      z = fmaf(w.lse, w.lse, z);
+      ++kept;
+      nan |= !(w.inv == w.inv);
     }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = nx[i];
+    on = on1;
+    on1 = on2;
+    r += kStep;
   }
   // the warp's rows, then the block's warps in order
 #pragma unroll
@@ -189,95 +239,90 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
 #pragma unroll
     for (int o = 16; o >= LPR; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     const int c = lig + LPR * i;
-    if (sub == 0 && c < E) psm[warp * E + c] = s;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    z += __shfl_xor_sync(0xffffffffu, z, o);
-    kept += __shfl_xor_sync(0xffffffffu, kept, o);
-  }
-  if (lane == 0) {
-    zred[warp] = z;
-    nred[warp] = kept;
+    if (sub == 0 && (FULL || c < E)) psm[warp * E + c] = s;
   }
   if (nan) bad = 1;
-  __syncthreads();
-  const float fix = __int_as_float((shift + 127) << 23);  // 2^shift
-  for (int e = tid; e < E; e += kThreads) {
+  z = block_sum(z, fred);
+  int nv = block_sum(kept, ired);  // its barriers also publish psm, hist and bad
+  bool poisoned = bad;
+  auto block_prob = [&](int e) {
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) s += psm[w * E + e];
-    if (s > 0.f)
-      atomicAdd(sc.psum + (size_t)seq * E + e, (unsigned long long)__float2ll_rn(s * fix));
-    if (hist[e]) atomicAdd(sc.cnt + (size_t)seq * E + e, hist[e]);
-  }
+    return s;
+  };
+
   uint32_t* head = sc.head + (size_t)seq * 4;
-  if (tid == 0) {
-    float s = 0.f;
-    int n = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      s += zred[w];
-      n += nred[w];
+  if (chunks > 1) {
+    const float fix = __int_as_float((shift + 127) << 23);  // 2^shift
+    for (int e = tid; e < E; e += kThreads) {
+      const float s = block_prob(e);
+      if (s > 0.f)
+        atomicAdd(sc.psum + (size_t)seq * E + e, (unsigned long long)__float2ll_rn(s * fix));
+      if (hist[e]) atomicAdd(sc.cnt + (size_t)seq * E + e, hist[e]);
     }
-    sc.zpart[blockIdx.x] = s;
-    atomicAdd(head, (uint32_t)n);
-    if (bad) atomicOr(head + 1, 1u);
+    if (tid == 0) {
+      sc.zpart[blockIdx.x] = z;
+      atomicAdd(head, (uint32_t)nv);
+      if (poisoned) atomicOr(head + 1, 1u);
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) last = atomicAdd(head + 2, 1u) == (uint32_t)(chunks - 1);
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    nv = (int)__ldcg(head);
+    poisoned = __ldcg(head + 1) != 0;
   }
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) last = atomicAdd(head + 2, 1u) == (uint32_t)(chunks - 1);
-  __syncthreads();
-  if (!last) return;
 
   // last block of the sequence: its outputs and its share of the losses
-  __threadfence();
-  const int nv = (int)__ldcg(head);
-  const float poison = __ldcg(head + 1) ? __int_as_float(0x7fffffff) : 0.f;
-  const double scale = nv ? ldexp(1.0, -shift) / (double)nv : 0.0;
-  const double fs = nv ? (double)E / ((double)K * (double)nv) : 0.0;
-  double part = 0.0;
+  const float poison = poisoned ? __int_as_float(0x7fffffff) : 0.f;
+  const float inv_n = nv ? 1.f / (float)nv : 0.f;
+  const float unfix = __int_as_float((127 - shift) << 23);  // 2^-shift
+  float part = 0.f;
   for (int e = tid; e < E; e += kThreads) {
     const size_t o = (size_t)seq * E + e;
-    const int c = __ldcg(sc.cnt + o);
-    const double p = (double)__ldcg(sc.psum + o) * scale;
+    int c;
+    float p;
+    if (chunks > 1) {
+      c = __ldcg(sc.cnt + o);
+      p = __ull2float_rn(__ldcg(sc.psum + o)) * unfix * inv_n;
+      sc.cnt[o] = 0;
+      sc.psum[o] = 0;
+    } else {
+      c = hist[e];
+      p = block_prob(e) * inv_n;
+    }
     counts[o] = c;
-    mean_prob[o] = (float)p + poison;
-    part += fs * (double)c * p;
-    sc.cnt[o] = 0;
-    sc.psum[o] = 0;
+    mean_prob[o] = p + poison;
+    part = fmaf((float)c, p, part);
   }
-  double zs = 0.0;
-  for (int i = tid; i < chunks; i += kThreads) {
-    float* zp = sc.zpart + (size_t)seq * chunks + i;
-    zs += (double)__ldcg(zp);
-    *zp = 0.f;
+  if (chunks > 1) {
+    z = 0.f;
+    for (int i = tid; i < chunks; i += kThreads) {
+      float* zp = sc.zpart + (size_t)seq * chunks + i;
+      z += __ldcg(zp);
+      *zp = 0.f;
+    }
+    z = block_sum(z, fred);
   }
-  auto block_sum2 = [&](double a, double b) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
+  const float bal = block_sum(part, fred) * ((float)E / (float)K) * inv_n + poison;
+  if (n_seq == 1) {
+    if (tid == 0) {
+      losses[0] = bal;
+      losses[1] = z * inv_n;
+      valid[0] = valid[1] = nv;
+      valid[2] = nv > 0;
+      if (chunks > 1) head[0] = head[1] = head[2] = 0;
     }
-    __syncthreads();
-    if (lane == 0) {
-      dred[0][warp] = a;
-      dred[1][warp] = b;
-    }
-    __syncthreads();
-    a = b = 0.0;
-    for (int w = 0; w < kWarps; ++w) {
-      a += dred[0][w];
-      b += dred[1][w];
-    }
-    return make_double2(a, b);
-  };
-  const double2 bz = block_sum2(part, zs);
+    return;
+  }
   if (tid == 0) {
-    sc.bal_seq[seq] = (float)bz.x + poison;
-    sc.z_seq[seq] = (float)bz.y;
+    sc.bal_seq[seq] = bal;
+    sc.z_seq[seq] = z;
     valid[seq] = nv;
-    head[0] = head[1] = head[2] = 0;
+    if (chunks > 1) head[0] = head[1] = head[2] = 0;
     __threadfence();
     last = atomicAdd(sc.done, 1u) == (uint32_t)(n_seq - 1);
   }
@@ -296,13 +341,15 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
     full += n > 0;
     sc.bal_seq[s] = sc.z_seq[s] = 0.f;
   }
-  const double2 lz = block_sum2(b, zz);
-  const double2 nf = block_sum2((double)total, (double)full);
+  b = block_sum(b, dred);
+  zz = block_sum(zz, dred);
+  total = block_sum(total, ired);
+  full = block_sum(full, ired);
   if (tid == 0) {
-    losses[0] = nf.y > 0.0 ? (float)(lz.x / nf.y) : 0.f;
-    losses[1] = nf.x > 0.0 ? (float)(lz.y / nf.x) : 0.f;
-    valid[n_seq] = (int)nf.x;
-    valid[n_seq + 1] = (int)nf.y;
+    losses[0] = full > 0 ? (float)b / (float)full : 0.f;
+    losses[1] = total > 0 ? (float)zz / (float)total : 0.f;
+    valid[n_seq] = total;
+    valid[n_seq + 1] = full;
     *sc.done = 0;
   }
 }
@@ -326,77 +373,65 @@ __global__ void balance_empty_kernel(int E, int n_seq, int32_t* __restrict__ cou
 }
 
 // ---------------------------------------------------------------- backward
-template <int LPR, int NPL, int MODE, bool AUX>
-__global__ void __launch_bounds__(kThreads)
+// Row stride of the per-row buffers in shared memory: the rows of a warp fall
+// into different banks.
+__host__ __device__ constexpr int buf_stride(int E, int lpr) { return (E + 31) / 32 * 32 + lpr; }
+
+// AUX: with the losses' gradient (reads the whole row of logits).
+template <int LPR, int NPL, int MODE, bool AUX, bool FULL>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(NPL))
 route_backward_kernel(RouteBackwardArgs a, int L, int chunks, int rows_per_block) {
   constexpr int RPW = 32 / LPR;
   constexpr int KPL = 32 / LPR;  // replicas of a token per lane, K <= 32
+  constexpr int kStep = kWarps * RPW;
+  constexpr bool kSigmoid = MODE != MOE_SCORE_SOFTMAX_RENORM;
   extern __shared__ float smem[];
-  pdl_wait();
-  pdl_trigger();
   const int E = a.E, K = a.K;
   const int warp = warp_id(), lane = lane_id();
   const int lig = lane % LPR, sub = lane / LPR;
-  float* buf = smem + (size_t)(warp * RPW + sub) * E;  // the row's routing gradient; zero between rows
+  const bool routing = a.d_weights != nullptr;
+  // the row's routing gradient; zero between rows
+  float* buf = smem + (AUX ? E : 0) + (size_t)(warp * RPW + sub) * buf_stride(E, LPR);
   const int seq = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
   const int r0 = chunk * rows_per_block;
   const int r1 = min(L, r0 + rows_per_block);
   const size_t t0 = (size_t)seq * L;
-  if (a.d_weights)
+  if (routing)
     for (int c = lig; c < E; c += LPR) buf[c] = 0.f;
+  pdl_wait();
+  pdl_trigger();
 
-  float f[NPL];
+  const uint8_t* mrow = a.mask ? a.mask + t0 : nullptr;
+  auto kept_row = [&](int r) { return r < r1 && (!mrow || __ldg(mrow + r)); };
+  const float* base = a.logits + t0 * a.ld;
+  int r = r0 + warp * RPW + sub;
+  bool on = kept_row(r), on1 = kept_row(r + kStep);
+  float v[NPL];
+  if constexpr (AUX) load_row<LPR, NPL, FULL>(base + (size_t)r * a.ld, E, lig, on, v);
+
   float gz = 0.f;
-  if constexpr (AUX) {
+  if constexpr (AUX) {  // a_e of this sequence, shared by its rows
     const int nv = __ldg(a.valid + seq), total = __ldg(a.valid + a.n_seq),
               full = __ldg(a.valid + a.n_seq + 1);
-    const float gb = __ldg(a.grad_losses);
     gz = total > 0 ? 2.f * __ldg(a.grad_losses + 1) / (float)total : 0.f;
-    const float k = nv > 0 ? gb * (float)E / ((float)K * (float)nv) / ((float)nv * (float)full) : 0.f;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int c = lig + LPR * i;
-      f[i] = c < E ? k * (float)__ldg(a.counts + (size_t)seq * E + c) : 0.f;
-    }
+    const float k = nv > 0 ? __ldg(a.grad_losses) * (float)E / ((float)K * (float)nv) /
+                                 ((float)nv * (float)full)
+                           : 0.f;
+    for (int e = threadIdx.x; e < E; e += kThreads)
+      smem[e] = k * (float)__ldg(a.counts + (size_t)seq * E + e);
   }
-  const float inv_scale = MODE == MOE_SCORE_SOFTMAX_RENORM ? 1.f : a.scale != 0.f ? 1.f / a.scale : 0.f;
-  __syncwarp();
+  const float inv_scale = !kSigmoid ? 1.f : a.scale != 0.f ? 1.f / a.scale : 0.f;
+  __syncthreads();
 
-  for (int rb = r0 + warp * RPW; rb < r1; rb += kWarps * RPW) {
-    const int r = rb + sub;
+  for (int rb = r0 + warp * RPW; rb < r1; rb += kStep) {
     const size_t t = t0 + r;
     const bool in = r < r1;
-    const bool on = in && (!a.mask || __ldg(a.mask + t));
-    float d[NPL];
-    if constexpr (AUX) {
-      float v[NPL];
-      load_row<LPR, NPL>(a.logits + t * a.ld, E, lig, on, v);
-      Row<NPL> w;
-      row_probs<LPR, NPL, MODE>(v, w);
-      float dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) dot = fmaf(f[i], w.p[i], dot);
-      dot = group_sum<LPR>(dot);
-      const float zl = gz * w.lse;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        float g = w.p[i] * (f[i] - dot);
-        if constexpr (MODE == MOE_SCORE_SOFTMAX_RENORM) {
-          if (gz != 0.f) g = fmaf(zl, w.p[i], g);
-        } else {
-          g *= sigmoid_tail(v[i]);
-          if (gz != 0.f && w.sum != 0.f) g = fmaf(zl, expf(v[i] - w.lse), g);
-        }
-        d[i] = g;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) d[i] = 0.f;
-    }
-    if (a.d_weights) {
-      int id[KPL];
-      float wk[KPL], gk[KPL];
-      float dot = 0.f;
+    float nx[NPL];
+    if constexpr (AUX) load_row<LPR, NPL, FULL>(base + (size_t)(r + kStep) * a.ld, E, lig, on1, nx);
+    const bool on2 = kept_row(r + 2 * kStep);
+    int id[KPL];
+    float wk[KPL], gk[KPL];
+    if (routing) {
 #pragma unroll
       for (int j = 0; j < KPL; ++j) {
         const int k = lig + LPR * j;
@@ -404,76 +439,141 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks, int rows_per_block
         id[j] = have ? __ldg(a.ids + t * K + k) : -1;
         wk[j] = have ? __ldg(a.weights + t * K + k) : 0.f;
         gk[j] = have ? __ldg(a.d_weights + t * K + k) : 0.f;
-        if (have && (unsigned)id[j] >= (unsigned)E) {
+      }
+    }
+    float u[NPL];
+    RowSums w;
+    float dot = 0.f;
+    if constexpr (AUX) {
+      w = row_probs<LPR, NPL, MODE>(v, u);
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        const int c = lig + LPR * i;
+        u[i] *= w.inv;
+        if (FULL || c < E) dot = fmaf(smem[c], u[i], dot);
+      }
+      dot = group_sum<LPR>(dot);
+    }
+    if (routing) {
+      float wg = 0.f;
+      bool lost = false;
+      int* tag = reinterpret_cast<int*>(buf);
+#pragma unroll
+      for (int j = 0; j < KPL; ++j) {
+        if (on && lig + LPR * j < K && (unsigned)id[j] >= (unsigned)E) {
           moe_set_status(a.dev_status, MOE_DEV_BAD_EXPERT_ID);
           id[j] = -1;
         }
-        dot = fmaf(wk[j], gk[j], dot);
+        wg = fmaf(wk[j], gk[j], wg);
+        if (id[j] >= 0) tag[id[j]] = lig + LPR * j + 1;
       }
-      dot = group_sum<LPR>(dot) * inv_scale;
+      wg = group_sum<LPR>(wg) * inv_scale;
+      __syncwarp();
 #pragma unroll
       for (int j = 0; j < KPL; ++j) {
-        gk[j] = wk[j] * (gk[j] - dot);
-        if constexpr (MODE != MOE_SCORE_SOFTMAX_RENORM) {
-          if (id[j] >= 0) gk[j] *= sigmoid_tail(__ldg(a.logits + t * a.ld + id[j]));
-        }
-        // one replica after the other: a repeated id adds up, in k order
-        for (int o = 0; o < LPR && LPR * j + o < K; ++o) {
-          if (lig == o && id[j] >= 0) buf[id[j]] += gk[j];
-          __syncwarp();
+        gk[j] = wk[j] * (gk[j] - wg);
+        if (id[j] >= 0) {
+          lost |= tag[id[j]] != lig + LPR * j + 1;
+          if constexpr (kSigmoid && !AUX) gk[j] *= sigmoid_tail(__ldg(base + (size_t)r * a.ld + id[j]));
         }
       }
+      // top-K gives distinct ids: every replica found its own tag and the
+      // values go out together; a repeated id adds up in k order instead
+      if (!__any_sync(0xffffffffu, lost)) {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const int c = lig + LPR * i;
-        if (c < E) {
-          d[i] += buf[c];
-          buf[c] = 0.f;
-        }
+        for (int j = 0; j < KPL; ++j)
+          if (id[j] >= 0) buf[id[j]] = gk[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < KPL; ++j)
+          if (id[j] >= 0) buf[id[j]] = 0.f;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < KPL; ++j)
+          for (int o = 0; o < LPR && LPR * j + o < K; ++o) {
+            if (lig == o && id[j] >= 0) buf[id[j]] += gk[j];
+            __syncwarp();
+          }
       }
       __syncwarp();
     }
-    if (in) {
-      float* o = a.dlogits + t * a.ld_d;
+    const float zl = gz * w.lse, zm = w.inv_exp;
+    float* out = a.dlogits + t * a.ld_d;
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const int c = lig + LPR * i;
-        if (c < E) o[c] = on ? d[i] : 0.f;
+    for (int i = 0; i < NPL; ++i) {
+      const int c = lig + LPR * i;
+      if (!FULL && c >= E) continue;
+      float d = routing ? buf[c] : 0.f;
+      if constexpr (AUX && !kSigmoid) {
+        float g = smem[c] - dot;
+        if (gz != 0.f) g += zl;
+        d = fmaf(u[i], g, d);
+      } else if constexpr (AUX) {
+        d = fmaf(u[i], smem[c] - dot, d) * sigmoid_tail(v[i]);
+        if (gz != 0.f) d = fmaf(zl, exp_fast(v[i] - w.max) * zm, d);
       }
-      if (a.d_shared_gate && lig == 0) {
-        float g = 0.f;
-        if (on) {
-          const float l = __ldg(a.logits + t * a.ld + E);
-          const float ea = expf(-fabsf(l));
-          const float q = 1.f / (1.f + ea);
-          g = __ldg(a.d_shared_gate + t) * (ea * q * q);
-        }
-        o[E] = g;
-      }
+      if (in) out[c] = on ? d : 0.f;
     }
+    if (routing) {
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < KPL; ++j)
+        if (id[j] >= 0) buf[id[j]] = 0.f;
+      __syncwarp();
+    }
+    if (a.d_shared_gate && in && lig == 0) {
+      float g = 0.f;
+      if (on) {
+        const float l = __ldg(base + (size_t)r * a.ld + E);
+        const float ea = expf(-fabsf(l));
+        const float q = 1.f / (1.f + ea);
+        g = __ldg(a.d_shared_gate + t) * (ea * q * q);
+      }
+      out[E] = g;
+    }
+    if constexpr (AUX) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) v[i] = nx[i];
+    }
+    on = on1;
+    on1 = on2;
+    r += kStep;
   }
 }
 
 // ---------------------------------------------------------------- shapes
+// Lanes per row and columns per lane by E: a row never takes more lanes than
+// it can feed, and a lane never more than 32 columns.  E = 896 has its own
+// tier, as in the top-K.
+struct Shape {
+  int lpr, npl;
+};
+Shape shape_of(int E) {
+  if (E <= 32) return {8, 4};
+  if (E <= 64) return {8, 8};
+  if (E <= 128) return {8, 16};
+  if (E <= 256) return {16, 16};
+  if (E <= 512) return {32, 16};
+  if (E <= 896) return {32, 28};
+  return {32, 32};
+}
+
+// One wave of blocks over all sequences, at least one pass of the block's
+// warps each; a fixed SM count, so that the scratch size does not depend on
+// which device is current.
+constexpr int kGridSms = 152;
 struct Chunks {
   int chunks, rows;
 };
-
-// about four blocks per SM over all sequences, at least one pass of the
-// block's warps each; a fixed SM count, so that the scratch size does not
-// depend on which device is current
-constexpr int kGridSms = 152;
-Chunks chunks_of(int L, int n_seq, int rows_per_pass) {
-  const int most = moe_cdiv(4 * kGridSms, n_seq);
-  int rows = moe_cdiv(L, most);
-  rows = moe_cdiv(rows, rows_per_pass) * rows_per_pass;
+Chunks chunks_of(int L, int n_seq, int E) {
+  const Shape sh = shape_of(E);
+  const int pass = kWarps * (32 / sh.lpr);
+  const int most = moe_cdiv(blocks_per_sm(sh.npl) * kGridSms, n_seq);
   Chunks c;
-  c.rows = rows;
-  c.chunks = moe_cdiv(L, rows);
+  c.rows = moe_cdiv(moe_cdiv(L, most), pass) * pass;
+  c.chunks = moe_cdiv(L, c.rows);
   return c;
 }
-
-int rows_per_pass(int E) { return kWarps * (E <= 128 ? 4 : E <= 256 ? 2 : 1); }
 
 Scratch scratch_of(void* p, int E, int n_seq, int blocks, size_t* bytes) {
   char* b = static_cast<char*>(p);
@@ -496,33 +596,62 @@ Scratch scratch_of(void* p, int E, int n_seq, int blocks, size_t* bytes) {
   return s;
 }
 
-template <int LPR, int NPL, int MODE>
-cudaError_t run_balance(const float* logits, int ld, const int32_t* ids, const uint8_t* mask, int T,
-                        int E, int K, int n_seq, void* scratch, int32_t* counts, float* mean_prob,
-                        int32_t* valid, float* losses, int32_t* dev_status, cudaStream_t stream) {
-  const int L = T / n_seq;
-  const Chunks c = chunks_of(L, n_seq, rows_per_pass(E));
-  const Scratch s = scratch_of(scratch, E, n_seq, n_seq * c.chunks, nullptr);
+// Calls f<LPR, NPL, FULL> for the shape of E.
+#define MOE_BY_SHAPE(f, E, ...)                                                                  \
+  switch (shape_of(E).lpr * 64 + shape_of(E).npl) {                                              \
+    case 8 * 64 + 4: return (E) == 32 ? f<8, 4, true>(__VA_ARGS__) : f<8, 4, false>(__VA_ARGS__);     \
+    case 8 * 64 + 8: return (E) == 64 ? f<8, 8, true>(__VA_ARGS__) : f<8, 8, false>(__VA_ARGS__);     \
+    case 8 * 64 + 16: return (E) == 128 ? f<8, 16, true>(__VA_ARGS__) : f<8, 16, false>(__VA_ARGS__); \
+    case 16 * 64 + 16: return (E) == 256 ? f<16, 16, true>(__VA_ARGS__) : f<16, 16, false>(__VA_ARGS__); \
+    case 32 * 64 + 16: return (E) == 512 ? f<32, 16, true>(__VA_ARGS__) : f<32, 16, false>(__VA_ARGS__); \
+    case 32 * 64 + 28: return (E) == 896 ? f<32, 28, true>(__VA_ARGS__) : f<32, 28, false>(__VA_ARGS__); \
+    default: return (E) == 1024 ? f<32, 32, true>(__VA_ARGS__) : f<32, 32, false>(__VA_ARGS__);       \
+  }
+
+struct BalanceArgs {
+  const float* logits;
+  int ld;
+  const int32_t* ids;
+  const uint8_t* mask;
+  int T, E, K, n_seq, mode;
+  void* scratch;
+  int32_t* counts;
+  float* mean_prob;
+  int32_t* valid;
+  float* losses;
+  int32_t* dev_status;
+};
+
+template <int LPR, int NPL, bool FULL>
+cudaError_t run_balance(const BalanceArgs& a, cudaStream_t stream) {
+  const int L = a.T / a.n_seq;
+  const Chunks c = chunks_of(L, a.n_seq, a.E);
+  const Scratch s = scratch_of(a.scratch, a.E, a.n_seq, a.n_seq * c.chunks, nullptr);
   // L probabilities of at most 1 sum to at most 2^bits, so 2^61 in fixed point
   int bits = 0;
   while (bits < 31 && (1ll << bits) < L) ++bits;
-  const size_t smem = (size_t)(kWarps + 1) * E * 4;
-  return moe_launch(balance_kernel<LPR, NPL, MODE>, dim3(n_seq * c.chunks), dim3(kThreads), smem,
-                    stream, 1, logits, ld, ids, mask, L, E, K, n_seq, c.chunks, c.rows, 61 - bits,
-                    s, counts, mean_prob, valid, losses, dev_status);
+  const size_t smem = (size_t)(kWarps + 1) * a.E * 4;
+  auto k = a.mode == MOE_SCORE_SOFTMAX_RENORM
+               ? balance_kernel<LPR, NPL, MOE_SCORE_SOFTMAX_RENORM, FULL>
+               : balance_kernel<LPR, NPL, MOE_SCORE_SIGMOID_BIAS_SCALED, FULL>;
+  return moe_launch(k, dim3(a.n_seq * c.chunks), dim3(kThreads), smem, stream, 1, a.logits, a.ld,
+                    a.ids, a.mask, L, a.E, a.K, a.n_seq, c.chunks, c.rows, 61 - bits, s, a.counts,
+                    a.mean_prob, a.valid, a.losses, a.dev_status);
 }
 
-template <int LPR, int NPL>
+template <int LPR, int NPL, bool FULL>
 cudaError_t run_route_backward(const RouteBackwardArgs& a, cudaStream_t stream) {
   const int L = a.T / a.n_seq;
-  const Chunks c = chunks_of(L, a.n_seq, rows_per_pass(a.E));
-  const size_t smem = a.d_weights ? (size_t)kWarps * (32 / LPR) * a.E * 4 : 0;
+  const Chunks c = chunks_of(L, a.n_seq, a.E);
   const bool aux = a.grad_losses != nullptr;
-  auto k = a.mode == MOE_SCORE_SOFTMAX_RENORM
-               ? (aux ? route_backward_kernel<LPR, NPL, MOE_SCORE_SOFTMAX_RENORM, true>
-                      : route_backward_kernel<LPR, NPL, MOE_SCORE_SOFTMAX_RENORM, false>)
-               : (aux ? route_backward_kernel<LPR, NPL, MOE_SCORE_SIGMOID_BIAS_SCALED, true>
-                      : route_backward_kernel<LPR, NPL, MOE_SCORE_SIGMOID_BIAS_SCALED, false>);
+  const size_t smem =
+      4 * ((aux ? a.E : 0) +
+           (a.d_weights ? (size_t)kWarps * (32 / LPR) * buf_stride(a.E, LPR) : 0));
+  constexpr int S0 = MOE_SCORE_SOFTMAX_RENORM, S1 = MOE_SCORE_SIGMOID_BIAS_SCALED;
+  auto k = a.mode == S0 ? (aux ? route_backward_kernel<LPR, NPL, S0, true, FULL>
+                               : route_backward_kernel<LPR, NPL, S0, false, false>)
+                        : (aux ? route_backward_kernel<LPR, NPL, S1, true, FULL>
+                               : route_backward_kernel<LPR, NPL, S1, false, false>);
   return moe_launch(k, dim3(a.n_seq * c.chunks), dim3(kThreads), smem, stream, 1, a, L, c.chunks,
                     c.rows);
 }
@@ -531,7 +660,7 @@ cudaError_t run_route_backward(const RouteBackwardArgs& a, cudaStream_t stream) 
 
 size_t balance_loss_scratch_bytes(int T, int E, int n_seq) {
   const int L = T / n_seq;
-  const int chunks = L > 0 ? chunks_of(L, n_seq, rows_per_pass(E)).chunks : 1;
+  const int chunks = L > 0 ? chunks_of(L, n_seq, E).chunks : 1;
   size_t bytes = 0;
   scratch_of(nullptr, E, n_seq, n_seq * chunks, &bytes);
   return bytes;
@@ -547,30 +676,11 @@ cudaError_t launch_balance_loss(const float* logits, int ld, const int32_t* ids,
     return moe_launch(balance_empty_kernel, dim3(grid), dim3(256), 0, stream, 1, E, n_seq, counts,
                       mean_prob, valid, losses);
   }
-#define MOE_BALANCE(LPR, NPL)                                                                      \
-  return mode == MOE_SCORE_SOFTMAX_RENORM                                                          \
-             ? run_balance<LPR, NPL, MOE_SCORE_SOFTMAX_RENORM>(logits, ld, ids, mask, T, E, K,     \
-                                                               n_seq, scratch, counts, mean_prob,  \
-                                                               valid, losses, dev_status, stream)  \
-             : run_balance<LPR, NPL, MOE_SCORE_SIGMOID_BIAS_SCALED>(                               \
-                   logits, ld, ids, mask, T, E, K, n_seq, scratch, counts, mean_prob, valid,       \
-                   losses, dev_status, stream)
-  if (E <= 32) MOE_BALANCE(8, 4);
-  if (E <= 64) MOE_BALANCE(8, 8);
-  if (E <= 128) MOE_BALANCE(8, 16);
-  if (E <= 256) MOE_BALANCE(16, 16);
-  if (E <= 512) MOE_BALANCE(32, 16);
-  if (E <= 896) MOE_BALANCE(32, 28);
-  MOE_BALANCE(32, 32);
-#undef MOE_BALANCE
+  const BalanceArgs a{logits, ld,      ids,    mask,      T,     E,      K,         n_seq,
+                      mode,   scratch, counts, mean_prob, valid, losses, dev_status};
+  MOE_BY_SHAPE(run_balance, E, a, stream)
 }
 
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t stream) {
-  if (a.E <= 32) return run_route_backward<8, 4>(a, stream);
-  if (a.E <= 64) return run_route_backward<8, 8>(a, stream);
-  if (a.E <= 128) return run_route_backward<8, 16>(a, stream);
-  if (a.E <= 256) return run_route_backward<16, 16>(a, stream);
-  if (a.E <= 512) return run_route_backward<32, 16>(a, stream);
-  if (a.E <= 896) return run_route_backward<32, 28>(a, stream);
-  return run_route_backward<32, 32>(a, stream);
+  MOE_BY_SHAPE(run_route_backward, a.E, a, stream)
 }
