@@ -19,6 +19,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "sm100_ptx.cuh"
 
 namespace {
 
@@ -74,17 +75,33 @@ MOE_DEVICE uint32_t amax8(const float* f) {
   return m;
 }
 
-// eight e4m3 codes of f / sc (0 where the whole group is zero)
+// Eight e4m3 codes of f / sc (0 where the whole group is zero).  The quotients
+// are IEEE's: with r = RN(1 / sc) and q = RN(f r), RN(q + r (f - q sc)) is the
+// correctly rounded quotient (Markstein's theorem) while nothing leaves the
+// normal range, which scales within 2^+-80 see to -- |f / sc| is at most 448.
+// Three operations per value where the division takes about ten.
 MOE_DEVICE uint2 codes8(const float* f, float sc) {
   if (sc == 0.f) return make_uint2(0u, 0u);
+  float q[8];
+  if (sc > 0x1p-80f && sc < 0x1p80f) {
+    const float r = __frcp_rn(sc);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q0 = f[i] * r;
+      q[i] = fmaf(fmaf(-q0, sc, f[i]), r, q0);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(f[i], sc);
+  }
   uint32_t w[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float2 a = make_float2(__fdiv_rn(f[4 * h], sc), __fdiv_rn(f[4 * h + 1], sc));
-    const float2 b = make_float2(__fdiv_rn(f[4 * h + 2], sc), __fdiv_rn(f[4 * h + 3], sc));
-    w[h] = (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
-           (uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16;
-  }
+  for (int h = 0; h < 2; ++h)
+    w[h] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[4 * h], q[4 * h + 1]), __NV_SATFINITE,
+                                              __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[4 * h + 2], q[4 * h + 3]),
+                                              __NV_SATFINITE, __NV_E4M3)
+               << 16;
   return make_uint2(w[0], w[1]);
 }
 
@@ -168,76 +185,139 @@ add_rmsnorm_kernel(const uint4* x, const uint4* residual, const void* __restrict
   }
 }
 
-// Persistent over rows: a thread keeps its columns' weight gradient in
-// registers and writes one fp32 partial row per row slot at the end.
-template <int VPT, int MAXT, bool W32>
-__global__ void __launch_bounds__(MAXT)
+// Persistent over row groups of rpb rows, one row per tpr threads.  A thread
+// keeps its columns' weight gradient in registers; its vectors of the next
+// S - 1 groups are on their way into a ring in shared memory that only the
+// thread itself reads, so the copies need no barrier -- one barrier per group,
+// for the rows' dot products, is all.  At the end the block's rows are added
+// and one fp32 partial row is written.
+template <int VPT, int S, int BPS, bool W32>
+__global__ void __launch_bounds__(512, BPS)
 rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restrict__ h,
-                        const float* __restrict__ rstd, const void* __restrict__ w, long long T,
-                        int H8, float inv_h, int tpr, uint4* dx, float* __restrict__ part) {
+                        const float* __restrict__ rstd, const void* __restrict__ w, int T, int H8,
+                        float inv_h, int tpr, uint4* dx, float* __restrict__ part) {
+  extern __shared__ uint4 ring[];  // [S][3][VPT][blockDim.x]
   __shared__ float red[2][kMaxWarps];
+  const int nt = blockDim.x;
+  const int rpb = nt / tpr, rs = threadIdx.x / tpr, lt = threadIdx.x % tpr;
+  const int wpr = tpr >> 5;
+  const int groups = (T + rpb - 1) / rpb;
   pdl_wait();
   pdl_trigger();
-  const int rpb = blockDim.x / tpr;
-  const int lt = threadIdx.x % tpr;
-  const long long slot = (long long)blockIdx.x * rpb + threadIdx.x / tpr;
-  const long long slots = (long long)gridDim.x * rpb;
-  float dw[VPT][8];
+  auto slot_of = [&](int st, int arr, int j) { return ring + ((st * 3 + arr) * VPT + j) * nt + threadIdx.x; };
+  auto issue = [&](int g, int st) {
+    if (g < groups) {
+      const long long t = (long long)g * rpb + rs;
 #pragma unroll
-  for (int j = 0; j < VPT; ++j)
+      for (int j = 0; j < VPT; ++j) {
+        const int c = lt + tpr * j;
+        const bool in = c < H8 && t < T;
+        const size_t o = in ? (size_t)t * H8 + c : 0;
+        moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 0, j)), dy + o, in ? 16 : 0);
+        moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 1, j)), h + o, in ? 16 : 0);
+        if (dh) moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 2, j)), dh + o, in ? 16 : 0);
+      }
+    }
+    moe_ptx::cp_async_commit();
+  };
+  auto row_rstd = [&](int g) {
+    const long long t = (long long)g * rpb + rs;
+    return g < groups && t < T ? __ldg(rstd + t) : 0.f;
+  };
+  constexpr bool kKeepW = VPT <= 1;  // the weight stays in registers where they suffice
+  float dw[VPT][8], wk[kKeepW ? VPT : 1][8];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) dw[j][q] = 0.f;
-  int it = 0;
-  for (long long t = slot; t < T; t += slots, it ^= 1) {
-    const size_t base = (size_t)t * H8;
-    uint4 g[VPT], v[VPT], e[VPT];
+    if constexpr (kKeepW) {
+      if (lt + tpr * j < H8) load_weight8<W32>(w, lt + tpr * j, wk[j]);
+      else
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = lt + tpr * j;
-      const bool in = c < H8;
-      g[j] = in ? dy[base + c] : make_uint4(0u, 0u, 0u, 0u);
-      v[j] = in ? __ldg(h + base + c) : make_uint4(0u, 0u, 0u, 0u);
-      e[j] = in && dh ? dh[base + c] : make_uint4(0u, 0u, 0u, 0u);
+        for (int q = 0; q < 8; ++q) wk[j][q] = 0.f;
     }
-    const float s = __ldg(rstd + t);
+  }
+  int g = blockIdx.x;
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(g + i * gridDim.x, i);
+  float s = row_rstd(g);
+  for (int it = 0; g < groups; ++it, g += gridDim.x) {
+    issue(g + (S - 1) * gridDim.x, (it + S - 1) % S);
+    const float s_next = row_rstd(g + gridDim.x);
+    moe_ptx::cp_async_wait<S - 1>();
+    const int st = it % S;
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int c = lt + tpr * j;
-      if (c >= H8) continue;
+      if (lt + tpr * j >= H8) continue;
       float gf[8], hf[8], wf[8];
-      bf16x8_to_f32(g[j], gf);
-      bf16x8_to_f32(v[j], hf);
-      load_weight8<W32>(w, c, wf);
+      bf16x8_to_f32(*slot_of(st, 0, j), gf);
+      bf16x8_to_f32(*slot_of(st, 1, j), hf);
+      if constexpr (!kKeepW) load_weight8<W32>(w, lt + tpr * j, wf);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const float n = hf[q] * s;
         dw[j][q] = fmaf(gf[q], n, dw[j][q]);
-        dot = fmaf(gf[q] * wf[q], n, dot);
+        dot = fmaf(gf[q] * (kKeepW ? wk[kKeepW ? j : 0][q] : wf[q]), n, dot);
       }
     }
-    const float c1 = row_sum(dot, tpr, red, it) * inv_h;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (wpr > 1) {
+      if (lane_id() == 0) red[it & 1][warp_id()] = dot;
+      __syncthreads();
+      dot = lane_id() < wpr ? red[it & 1][rs * wpr + lane_id()] : 0.f;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      dot = __shfl_sync(0xffffffffu, dot, 0);
+    }
+    const float c1 = dot * inv_h * s;
+    const long long t = (long long)g * rpb + rs;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = lt + tpr * j;
+      if (c >= H8 || t >= T) continue;
+      float gf[8], hf[8], wf[8], ef[8], o[8];
+      bf16x8_to_f32(*slot_of(st, 0, j), gf);
+      bf16x8_to_f32(*slot_of(st, 1, j), hf);
+      bf16x8_to_f32(dh ? *slot_of(st, 2, j) : make_uint4(0u, 0u, 0u, 0u), ef);
+      if constexpr (!kKeepW) load_weight8<W32>(w, c, wf);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        o[q] = fmaf(s, fmaf(-hf[q], c1, gf[q] * (kKeepW ? wk[kKeepW ? j : 0][q] : wf[q])), ef[q]);
+      dx[(size_t)t * H8 + c] = pack8(o);
+    }
+    s = s_next;
+  }
+  float4* p = reinterpret_cast<float4*>(part) + (size_t)blockIdx.x * H8 * 2;
+  if (rpb == 1) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = lt + tpr * j;
       if (c >= H8) continue;
-      float gf[8], hf[8], wf[8], ef[8], o[8];
-      bf16x8_to_f32(g[j], gf);
-      bf16x8_to_f32(v[j], hf);
-      bf16x8_to_f32(e[j], ef);
-      load_weight8<W32>(w, c, wf);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) o[q] = fmaf(s, fmaf(-hf[q] * s, c1, gf[q] * wf[q]), ef[q]);
-      dx[base + c] = pack8(o);
+      p[2 * c] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+      p[2 * c + 1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
     }
+    return;
   }
-  float4* p = reinterpret_cast<float4*>(part + (size_t)slot * H8 * 8);
+  moe_ptx::cp_async_wait<0>();
+  __syncthreads();  // the ring takes the rows' sums: [rpb][H8 * 2] float4
+  float4* sums = reinterpret_cast<float4*>(ring);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int c = lt + tpr * j;
     if (c >= H8) continue;
-    p[2 * c] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-    p[2 * c + 1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+    sums[(rs * H8 + c) * 2] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+    sums[(rs * H8 + c) * 2 + 1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < H8 * 2; i += nt) {
+    float4 v = sums[i];
+    for (int r = 1; r < rpb; ++r) {
+      const float4 x = sums[r * H8 * 2 + i];
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    p[i] = v;
   }
 }
 
@@ -277,15 +357,26 @@ RowShape row_shape(int H8) {
   return r;
 }
 
-// fixed, not asked of the device: the scratch size must not depend on which
-// device is current
+// Backward: as few vectors per thread as 512 threads allow, as many rows per
+// block as fill them (fewer where the rows are too few to go round the SMs).
+// The SM count is fixed, not asked of the device: the scratch size must not
+// depend on which device is current.
 constexpr int kGridSms = 152;
-
-int backward_grid(long long T, const RowShape& r) {
-  const long long need = (T + r.rpb - 1) / r.rpb;
-  const int threads = r.tpr * r.rpb;
-  const long long full = (long long)kGridSms * (threads <= 512 ? 512 / threads : 1);
-  return (int)(need < full ? need : full);
+struct BackShape {
+  int vpt, tpr, rpb, grid;
+};
+BackShape back_shape(int T, int H8) {
+  BackShape r;
+  r.vpt = H8 <= 512 ? 1 : H8 <= 1024 ? 2 : H8 <= 2048 ? 4 : 8;
+  r.tpr = moe_cdiv(H8, 32 * r.vpt) * 32;
+  const int bps = r.vpt <= 2 ? 2 : 1;
+  int rpb = 512 / r.tpr;
+  const int share = moe_cdiv(T, bps * kGridSms);
+  if (rpb > share) rpb = share;
+  r.rpb = rpb < 1 ? 1 : rpb;
+  const int groups = moe_cdiv(T, r.rpb);
+  r.grid = groups < bps * kGridSms ? groups : bps * kGridSms;
+  return r;
 }
 
 struct NormArgs {
@@ -315,12 +406,20 @@ cudaError_t run_norm_q(int q, bool w32, const RowShape& r, const NormArgs& a, cu
                       : run_norm<VPT, MAXT, kQNone>(w32, r, a, s);
 }
 
-template <int VPT, int MAXT>
-cudaError_t run_backward(bool w32, const RowShape& r, int grid, const void* dy, const void* dh,
-                         const void* h, const float* rstd, const void* w, long long T, int H,
-                         void* dx, float* part, cudaStream_t stream) {
-  auto k = w32 ? rmsnorm_backward_kernel<VPT, MAXT, true> : rmsnorm_backward_kernel<VPT, MAXT, false>;
-  return moe_launch(k, dim3(grid), dim3(r.tpr * r.rpb), 0, stream, 1,
+template <int VPT, int S, int BPS>
+cudaError_t run_backward(bool w32, const BackShape& r, const void* dy, const void* dh,
+                         const void* h, const float* rstd, const void* w, int T, int H, void* dx,
+                         float* part, cudaStream_t stream) {
+  auto k = w32 ? rmsnorm_backward_kernel<VPT, S, BPS, true> : rmsnorm_backward_kernel<VPT, S, BPS, false>;
+  const int threads = r.tpr * r.rpb;
+  // the ring, or the rows' sums at the end
+  size_t smem = (size_t)S * 3 * VPT * threads * 16;
+  const size_t sums = r.rpb > 1 ? (size_t)r.rpb * H * 4 : 0;
+  if (smem < sums) smem = sums;
+  static std::atomic<unsigned long long> set[2];
+  cudaError_t e = moe_raise_smem(k, (size_t)S * 3 * VPT * 512 * 16, set[w32]);
+  if (e != cudaSuccess) return e;
+  return moe_launch(k, dim3(r.grid), dim3(threads), smem, stream, 1,
                     static_cast<const uint4*>(dy), static_cast<const uint4*>(dh),
                     static_cast<const uint4*>(h), rstd, w, T, H / 8, 1.f / (float)H, r.tpr,
                     static_cast<uint4*>(dx), part);
@@ -343,8 +442,8 @@ cudaError_t launch_add_rmsnorm(const void* x, const void* residual, const void* 
 }
 
 size_t add_rmsnorm_backward_scratch_bytes(int T, int H) {
-  const RowShape r = row_shape(H / 8);
-  return moe_align_up((size_t)backward_grid(T, r) * r.rpb * H * sizeof(float), 256);
+  const int rows = T > 0 ? back_shape(T, H / 8).grid : 1;
+  return moe_align_up((size_t)rows * H * sizeof(float), 256);
 }
 
 cudaError_t launch_add_rmsnorm_backward(const void* dy, const void* dh, const void* h,
@@ -354,15 +453,14 @@ cudaError_t launch_add_rmsnorm_backward(const void* dy, const void* dh, const vo
   float* part = static_cast<float*>(scratch);
   int rows = 0;
   if (T > 0) {
-    const RowShape r = row_shape(H / 8);
-    const int grid = backward_grid(T, r);
-    rows = grid * r.rpb;
+    const BackShape r = back_shape(T, H / 8);
+    rows = r.grid;
     cudaError_t e;
-    switch (r.vpt) {
-      case 1: e = run_backward<1, 256>(w32, r, grid, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
-      case 2: e = run_backward<2, 256>(w32, r, grid, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
-      case 4: e = run_backward<4, 256>(w32, r, grid, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
-      default: e = run_backward<8, 512>(w32, r, grid, dy, dh, h, rstd, w, T, H, dx, part, stream);
+    switch (r.vpt) {  // stages: what about 200 KB of shared memory per SM hold
+      case 1: e = run_backward<1, 4, 2>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
+      case 2: e = run_backward<2, 2, 2>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
+      case 4: e = run_backward<4, 2, 1>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
+      default: e = run_backward<8, 1, 1>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream);
     }
     if (e != cudaSuccess) return e;
   }
