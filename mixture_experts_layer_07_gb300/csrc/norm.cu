@@ -185,19 +185,59 @@ add_rmsnorm_kernel(const uint4* x, const uint4* residual, const void* __restrict
   }
 }
 
+// two fp32 products (and additions) in one instruction
+MOE_DEVICE float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+MOE_DEVICE float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+MOE_DEVICE float2 pair(float a) { return make_float2(a, a); }
+MOE_DEVICE void unpack4(const uint4& v, float2* f) {
+  f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+  f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+  f[2] = make_float2(bf16_lo(v.z), bf16_hi(v.z));
+  f[3] = make_float2(bf16_lo(v.w), bf16_hi(v.w));
+}
+template <bool W32>
+MOE_DEVICE void weight4(const void* w, int vec, float2* f) {
+  if constexpr (W32) {
+    const float4* p = reinterpret_cast<const float4*>(w) + 2 * (size_t)vec;
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    f[0] = make_float2(a.x, a.y); f[1] = make_float2(a.z, a.w);
+    f[2] = make_float2(b.x, b.y); f[3] = make_float2(b.z, b.w);
+  } else {
+    unpack4(__ldg(reinterpret_cast<const uint4*>(w) + vec), f);
+  }
+}
+
 // Persistent over row groups of rpb rows, one row per tpr threads.  A thread
-// keeps its columns' weight gradient in registers; its vectors of the next
-// S - 1 groups are on their way into a ring in shared memory that only the
-// thread itself reads, so the copies need no barrier -- one barrier per group,
-// for the rows' dot products, is all.  At the end the block's rows are added
-// and one fp32 partial row is written.
-template <int VPT, int S, int BPS, bool W32>
-__global__ void __launch_bounds__(512, BPS)
+// keeps its columns' weight gradient in registers.  Its vectors of the next
+// row groups are on their way into a ring of S stages in shared memory that
+// only the thread itself reads, so the copies need no barrier; the rows' dot
+// products take one barrier per group.  With LAG, a group's dx is computed one
+// group late, behind the next group's sums, so that no warp waits at the
+// barrier with nothing to do.  At the end the block's rows are added and one
+// fp32 partial row is written.
+template <int VPT, int S, int MAXT, bool LAG, bool W32>
+__global__ void __launch_bounds__(MAXT, 1)
 rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restrict__ h,
                         const float* __restrict__ rstd, const void* __restrict__ w, int T, int H8,
                         float inv_h, int tpr, uint4* dx, float* __restrict__ part) {
-  extern __shared__ uint4 ring[];  // [S][3][VPT][blockDim.x]
-  __shared__ float red[2][kMaxWarps];
+  constexpr int kAhead = LAG ? S - 2 : S - 1;  // groups in flight behind the current one
+  extern __shared__ uint4 ring[];              // [S][3][VPT][blockDim.x]
+  __shared__ float red[2][MAXT / 32];
   const int nt = blockDim.x;
   const int rpb = nt / tpr, rs = threadIdx.x / tpr, lt = threadIdx.x % tpr;
   const int wpr = tpr >> 5;
@@ -206,16 +246,16 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restric
   pdl_trigger();
   auto slot_of = [&](int st, int arr, int j) { return ring + ((st * 3 + arr) * VPT + j) * nt + threadIdx.x; };
   auto issue = [&](int g, int st) {
-    if (g < groups) {
-      const long long t = (long long)g * rpb + rs;
+    const long long t = (long long)g * rpb + rs;
+    if (g < groups && t < T) {
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         const int c = lt + tpr * j;
-        const bool in = c < H8 && t < T;
-        const size_t o = in ? (size_t)t * H8 + c : 0;
-        moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 0, j)), dy + o, in ? 16 : 0);
-        moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 1, j)), h + o, in ? 16 : 0);
-        if (dh) moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 2, j)), dh + o, in ? 16 : 0);
+        if (c >= H8) continue;
+        const size_t o = (size_t)t * H8 + c;
+        moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 0, j)), dy + o, 16);
+        moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 1, j)), h + o, 16);
+        if (dh) moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 2, j)), dh + o, 16);
       }
     }
     moe_ptx::cp_async_commit();
@@ -224,93 +264,99 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restric
     const long long t = (long long)g * rpb + rs;
     return g < groups && t < T ? __ldg(rstd + t) : 0.f;
   };
-  constexpr bool kKeepW = VPT <= 1;  // the weight stays in registers where they suffice
-  float dw[VPT][8], wk[kKeepW ? VPT : 1][8];
+  constexpr bool kKeepW = VPT == 1;  // the weight stays in registers where they suffice
+  float2 dw[VPT][4], wk[4];
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) {
+  for (int j = 0; j < VPT; ++j)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) dw[j][q] = 0.f;
-    if constexpr (kKeepW) {
-      if (lt + tpr * j < H8) load_weight8<W32>(w, lt + tpr * j, wk[j]);
-      else
-#pragma unroll
-        for (int q = 0; q < 8; ++q) wk[j][q] = 0.f;
-    }
-  }
-  int g = blockIdx.x;
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(g + i * gridDim.x, i);
-  float s = row_rstd(g);
-  for (int it = 0; g < groups; ++it, g += gridDim.x) {
-    issue(g + (S - 1) * gridDim.x, (it + S - 1) % S);
-    const float s_next = row_rstd(g + gridDim.x);
-    moe_ptx::cp_async_wait<S - 1>();
-    const int st = it % S;
-    float dot = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (lt + tpr * j >= H8) continue;
-      float gf[8], hf[8], wf[8];
-      bf16x8_to_f32(*slot_of(st, 0, j), gf);
-      bf16x8_to_f32(*slot_of(st, 1, j), hf);
-      if constexpr (!kKeepW) load_weight8<W32>(w, lt + tpr * j, wf);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float n = hf[q] * s;
-        dw[j][q] = fmaf(gf[q], n, dw[j][q]);
-        dot = fmaf(gf[q] * (kKeepW ? wk[kKeepW ? j : 0][q] : wf[q]), n, dot);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (wpr > 1) {
-      if (lane_id() == 0) red[it & 1][warp_id()] = dot;
-      __syncthreads();
-      dot = lane_id() < wpr ? red[it & 1][rs * wpr + lane_id()] : 0.f;
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      dot = __shfl_sync(0xffffffffu, dot, 0);
-    }
-    const float c1 = dot * inv_h * s;
+    for (int q = 0; q < 4; ++q) dw[j][q] = pair(0.f);
+  if (kKeepW && lt < H8) weight4<W32>(w, lt, wk);
+
+  // dx of group g, whose rows lie in stage st and whose dot products in red[slot]
+  auto finish = [&](int g, int st, int slot, float s, float dot) {
     const long long t = (long long)g * rpb + rs;
+    if (wpr > 1) {
+      dot = lane_id() < wpr ? red[slot][rs * wpr + lane_id()] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    }
+    const float c1 = -(dot * inv_h) * s;  // dx = s (dy w + h c1) + dh
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = lt + tpr * j;
       if (c >= H8 || t >= T) continue;
-      float gf[8], hf[8], wf[8], ef[8], o[8];
-      bf16x8_to_f32(*slot_of(st, 0, j), gf);
-      bf16x8_to_f32(*slot_of(st, 1, j), hf);
-      bf16x8_to_f32(dh ? *slot_of(st, 2, j) : make_uint4(0u, 0u, 0u, 0u), ef);
-      if constexpr (!kKeepW) load_weight8<W32>(w, c, wf);
+      float2 gf[4], hf[4], wf[4], ef[4], o[4];
+      unpack4(*slot_of(st, 0, j), gf);
+      unpack4(*slot_of(st, 1, j), hf);
+      unpack4(dh ? *slot_of(st, 2, j) : make_uint4(0u, 0u, 0u, 0u), ef);
+      if constexpr (!kKeepW) weight4<W32>(w, c, wf);
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        o[q] = fmaf(s, fmaf(-hf[q], c1, gf[q] * (kKeepW ? wk[kKeepW ? j : 0][q] : wf[q])), ef[q]);
-      dx[(size_t)t * H8 + c] = pack8(o);
+      for (int q = 0; q < 4; ++q)
+        o[q] = fma2(pair(s), fma2(hf[q], pair(c1), mul2(gf[q], kKeepW ? wk[q] : wf[q])), ef[q]);
+      dx[(size_t)t * H8 + c] = make_uint4(pack_bf16x2(o[0].x, o[0].y), pack_bf16x2(o[1].x, o[1].y),
+                                          pack_bf16x2(o[2].x, o[2].y), pack_bf16x2(o[3].x, o[3].y));
     }
+  };
+
+  int g = blockIdx.x;
+  const int step = gridDim.x;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) issue(g + i * step, i);
+  float s = row_rstd(g), s_prev = 0.f, dot_prev = 0.f;
+  int it = 0;
+  for (; g < groups; ++it, g += step) {
+    issue(g + kAhead * step, (it + kAhead) % S);
+    const float s_next = row_rstd(g + step);
+    moe_ptx::cp_async_wait<kAhead>();
+    const int st = it % S;
+    float2 dot2 = pair(0.f);
+    if ((long long)g * rpb + rs < T) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        if (lt + tpr * j >= H8) continue;
+        float2 gf[4], hf[4], wf[4];
+        unpack4(*slot_of(st, 0, j), gf);
+        unpack4(*slot_of(st, 1, j), hf);
+        if constexpr (!kKeepW) weight4<W32>(w, lt + tpr * j, wf);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 n = mul2(hf[q], pair(s));
+          dw[j][q] = fma2(gf[q], n, dw[j][q]);
+          dot2 = fma2(mul2(gf[q], kKeepW ? wk[q] : wf[q]), n, dot2);
+        }
+      }
+    }
+    float dot = dot2.x + dot2.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (wpr > 1 && lane_id() == 0) red[it & 1][warp_id()] = dot;
+    if (LAG && it > 0) finish(g - step, (it - 1) % S, (it - 1) & 1, s_prev, dot_prev);
+    if (wpr > 1) __syncthreads();
+    if (!LAG) finish(g, st, it & 1, s, dot);
+    s_prev = s;
+    dot_prev = dot;
     s = s_next;
   }
+  if (LAG && it > 0) finish(g - step, (it - 1) % S, (it - 1) & 1, s_prev, dot_prev);
+
   float4* p = reinterpret_cast<float4*>(part) + (size_t)blockIdx.x * H8 * 2;
-  if (rpb == 1) {
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = lt + tpr * j;
-      if (c >= H8) continue;
-      p[2 * c] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-      p[2 * c + 1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
-    }
-    return;
+  // one row per block: its sums are the block's; else they meet in the ring,
+  // as [rpb][H8 * 2] float4
+  float4* sums = rpb == 1 ? p : reinterpret_cast<float4*>(ring) + (size_t)rs * H8 * 2;
+  if (rpb > 1) {
+    moe_ptx::cp_async_wait<0>();
+    __syncthreads();
   }
-  moe_ptx::cp_async_wait<0>();
-  __syncthreads();  // the ring takes the rows' sums: [rpb][H8 * 2] float4
-  float4* sums = reinterpret_cast<float4*>(ring);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int c = lt + tpr * j;
     if (c >= H8) continue;
-    sums[(rs * H8 + c) * 2] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-    sums[(rs * H8 + c) * 2 + 1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+    sums[c * 2] = make_float4(dw[j][0].x, dw[j][0].y, dw[j][1].x, dw[j][1].y);
+    sums[c * 2 + 1] = make_float4(dw[j][2].x, dw[j][2].y, dw[j][3].x, dw[j][3].y);
   }
+  if (rpb == 1) return;
   __syncthreads();
+  sums = reinterpret_cast<float4*>(ring);
   for (int i = threadIdx.x; i < H8 * 2; i += nt) {
     float4 v = sums[i];
     for (int r = 1; r < rpb; ++r) {
@@ -330,8 +376,10 @@ column_sum_kernel(const float* __restrict__ part, int rows, int H, float* __rest
   pdl_trigger();
   const int c = blockIdx.x * 32 + lane_id();
   float s = 0.f;
-  if (c < H)
+  if (c < H) {
+#pragma unroll 8
     for (int r = warp_id(); r < rows; r += 32) s += __ldg(part + (size_t)r * H + c);
+  }
   red[warp_id()][lane_id()] = s;
   __syncthreads();
   if (warp_id() == 0 && c < H) {
@@ -357,25 +405,23 @@ RowShape row_shape(int H8) {
   return r;
 }
 
-// Backward: as few vectors per thread as 512 threads allow, as many rows per
-// block as fill them (fewer where the rows are too few to go round the SMs).
-// The SM count is fixed, not asked of the device: the scratch size must not
-// depend on which device is current.
+// Backward: one vector per thread up to 1024 threads (H <= 8192), several
+// beyond; as many rows per block as fill the threads, fewer where the rows are
+// too few to go round the SMs.  The SM count is fixed, not asked of the device:
+// the scratch size must not depend on which device is current.
 constexpr int kGridSms = 152;
 struct BackShape {
   int vpt, tpr, rpb, grid;
 };
 BackShape back_shape(int T, int H8) {
   BackShape r;
-  r.vpt = H8 <= 512 ? 1 : H8 <= 1024 ? 2 : H8 <= 2048 ? 4 : 8;
+  r.vpt = H8 <= 1024 ? 1 : H8 <= 2048 ? 4 : 8;
   r.tpr = moe_cdiv(H8, 32 * r.vpt) * 32;
-  const int bps = r.vpt <= 2 ? 2 : 1;
-  int rpb = 512 / r.tpr;
-  const int share = moe_cdiv(T, bps * kGridSms);
-  if (rpb > share) rpb = share;
-  r.rpb = rpb < 1 ? 1 : rpb;
+  const int share = moe_cdiv(T, kGridSms);
+  const int fit = (r.vpt == 1 ? 1024 : 512) / r.tpr;
+  r.rpb = share < fit ? share : fit;
   const int groups = moe_cdiv(T, r.rpb);
-  r.grid = groups < bps * kGridSms ? groups : bps * kGridSms;
+  r.grid = groups < kGridSms ? groups : kGridSms;
   return r;
 }
 
@@ -406,20 +452,18 @@ cudaError_t run_norm_q(int q, bool w32, const RowShape& r, const NormArgs& a, cu
                       : run_norm<VPT, MAXT, kQNone>(w32, r, a, s);
 }
 
-template <int VPT, int S, int BPS>
+template <int VPT, int S, int MAXT, bool LAG>
 cudaError_t run_backward(bool w32, const BackShape& r, const void* dy, const void* dh,
                          const void* h, const float* rstd, const void* w, int T, int H, void* dx,
                          float* part, cudaStream_t stream) {
-  auto k = w32 ? rmsnorm_backward_kernel<VPT, S, BPS, true> : rmsnorm_backward_kernel<VPT, S, BPS, false>;
-  const int threads = r.tpr * r.rpb;
-  // the ring, or the rows' sums at the end
-  size_t smem = (size_t)S * 3 * VPT * threads * 16;
-  const size_t sums = r.rpb > 1 ? (size_t)r.rpb * H * 4 : 0;
-  if (smem < sums) smem = sums;
+  auto k = w32 ? rmsnorm_backward_kernel<VPT, S, MAXT, LAG, true>
+               : rmsnorm_backward_kernel<VPT, S, MAXT, LAG, false>;
+  constexpr size_t kPerThread = (size_t)S * 3 * VPT * 16;  // >= 32 VPT: the rows' sums fit
   static std::atomic<unsigned long long> set[2];
-  cudaError_t e = moe_raise_smem(k, (size_t)S * 3 * VPT * 512 * 16, set[w32]);
+  cudaError_t e = moe_raise_smem(k, kPerThread * MAXT, set[w32]);
   if (e != cudaSuccess) return e;
-  return moe_launch(k, dim3(r.grid), dim3(threads), smem, stream, 1,
+  const int threads = r.tpr * r.rpb;
+  return moe_launch(k, dim3(r.grid), dim3(threads), kPerThread * threads, stream, 1,
                     static_cast<const uint4*>(dy), static_cast<const uint4*>(dh),
                     static_cast<const uint4*>(h), rstd, w, T, H / 8, 1.f / (float)H, r.tpr,
                     static_cast<uint4*>(dx), part);
@@ -456,11 +500,10 @@ cudaError_t launch_add_rmsnorm_backward(const void* dy, const void* dh, const vo
     const BackShape r = back_shape(T, H / 8);
     rows = r.grid;
     cudaError_t e;
-    switch (r.vpt) {  // stages: what about 200 KB of shared memory per SM hold
-      case 1: e = run_backward<1, 4, 2>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
-      case 2: e = run_backward<2, 2, 2>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
-      case 4: e = run_backward<4, 2, 1>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
-      default: e = run_backward<8, 1, 1>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream);
+    switch (r.vpt) {  // 196 KB of ring each
+      case 1: e = run_backward<1, 4, 1024, true>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
+      case 4: e = run_backward<4, 2, 512, false>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
+      default: e = run_backward<8, 1, 512, false>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream);
     }
     if (e != cudaSuccess) return e;
   }
