@@ -56,7 +56,7 @@ moe_status_t check_norm(int T, int H, int weight_dtype) {
 // a routed batch of n_seq sequences of T / n_seq tokens
 moe_status_t check_router(int T, int E, int K, int n_seq, int mode) {
   if (T < 0 || E <= 0 || E > 1024 || K <= 0 || K > E || K > 32) return MOE_ERR_INVALID_ARG;
-  if (n_seq <= 0 || T % n_seq != 0 || (int64_t)T * K > 0x7fffffff) return MOE_ERR_INVALID_ARG;
+  if (n_seq <= 0 || T % n_seq != 0 || (int64_t)T * K > 0x7fffffff / 2) return MOE_ERR_INVALID_ARG;
   if (mode != MOE_SCORE_SOFTMAX_RENORM && mode != MOE_SCORE_SIGMOID_BIAS_SCALED)
     return MOE_ERR_INVALID_ARG;
   return MOE_OK;

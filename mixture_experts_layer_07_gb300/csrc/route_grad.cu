@@ -56,81 +56,73 @@ MOE_DEVICE float group_max(float v) {
   return v;
 }
 
-// e^x as one hardware 2^x: x is at most 0 wherever this is used, or cancels in
-// a ratio; its relative error is about |x| 2^-24 + 2^-22
-MOE_DEVICE float exp_fast(float x) {
+constexpr float kLog2E = 1.4426950408889634f;
+
+// Hardware 2^x (relative error about 2^-22; results below 2^-126 are 0) and,
+// for 1 <= x <= 2, 1 / x.
+MOE_DEVICE float ex2(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// 1 / x for 1 <= x <= 2
-MOE_DEVICE float rcp_fast(float x) {
+MOE_DEVICE float rcp(float x) {
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
 // 1 - sigmoid(l)
 MOE_DEVICE float sigmoid_tail(float l) {
-  const float a = exp_fast(-fabsf(l));
-  return (l > 0.f ? a : 1.f) * rcp_fast(1.f + a);
+  const float a = ex2(-fabsf(l) * kLog2E);
+  return (l > 0.f ? a : 1.f) * rcp(1.f + a);
 }
 
-// What a row's logits v turn into (-inf past E): weights u, their probabilities
-// u * inv, the maximum (0 for a row of -inf), log-sum-exp (0 for such a row)
-// and 1 / sum of e^(v - max) (0 for such a row).
-//   mode 0: u = e^(v - max)
-//   mode 1: u = sigmoid(v) e^c, c = max(0, -max): the common factor cancels in
-//           u * inv and keeps rows of very negative logits from vanishing
-struct RowSums {
-  float max, lse, inv, inv_exp;
-};
+// f(i, e^(v[i] - m)) for every column.  Folding m into one multiply-add rounds
+// m log2(e) once, a factor that all columns share: it cancels in a ratio and
+// shifts the sum's logarithm by at most |m| 2^-24.  Maxima past 10^4 -- rows of
+// the type's lowest value among them, where the folded product overflows --
+// take the difference first.
+template <int NPL, typename F>
+MOE_DEVICE void exp_row(const float (&v)[NPL], float m, F&& f) {
+  if (fabsf(m) <= 1e4f) {
+    const float ml = m * kLog2E;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) f(i, ex2(fmaf(v[i], kLog2E, -ml)));
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) f(i, ex2((v[i] - m) * kLog2E));
+  }
+}
 
-template <int LPR, int NPL, int MODE>
-MOE_DEVICE RowSums row_probs(const float (&v)[NPL], float (&u)[NPL]) {
+// The row's maximum, 0 where that is -inf (no expert is left).
+template <int LPR, int NPL>
+MOE_DEVICE float row_max(const float (&v)[NPL]) {
   float m = v[0];
 #pragma unroll
   for (int i = 1; i < NPL; ++i) m = fmaxf(m, v[i]);
   m = group_max<LPR>(m);
-  if (m == kNegInf) m = 0.f;
-  RowSums r;
-  r.max = m;
-  float s = 0.f;
-  if constexpr (MODE == MOE_SCORE_SOFTMAX_RENORM) {
+  return m == kNegInf ? 0.f : m;
+}
+
+// Mode 1: f(i, u) with u = sigmoid(v[i]) e^c, c = max(0, -m): the common
+// factor cancels in u / sum u and keeps rows of very negative logits from
+// vanishing.
+template <int NPL, typename F>
+MOE_DEVICE void sigmoid_row(const float (&v)[NPL], float m, F&& f) {
+  if (m >= 0.f) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      u[i] = exp_fast(v[i] - m);
-      s += u[i];
+      const float a = ex2(-fabsf(v[i]) * kLog2E);
+      f(i, (v[i] > 0.f ? 1.f : a) * rcp(1.f + a));
     }
-    s = group_sum<LPR>(s);
-  } else {
-    float q = 0.f;
-    if (m >= 0.f) {  // c = 0
+  } else {  // every logit is negative
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const float a = exp_fast(-fabsf(v[i]));
-        u[i] = (v[i] > 0.f ? 1.f : a) * rcp_fast(1.f + a);
-        s += exp_fast(v[i] - m);
-        q += u[i];
-      }
-    } else {  // every logit is negative
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const float e = exp_fast(v[i] - m);
-        u[i] = e * rcp_fast(1.f + exp_fast(v[i]));
-        s += e;
-        q += u[i];
-      }
-    }
-    s = group_sum<LPR>(s);
-    q = group_sum<LPR>(q);
-    r.inv = q == 0.f ? 0.f : 1.f / q;
+    for (int i = 0; i < NPL; ++i)
+      f(i, ex2((v[i] - m) * kLog2E) * rcp(1.f + ex2(v[i] * kLog2E)));
   }
-  r.lse = s == 0.f ? 0.f : m + logf(s);
-  r.inv_exp = s == 0.f ? 0.f : 1.f / s;
-  if constexpr (MODE == MOE_SCORE_SOFTMAX_RENORM) r.inv = r.inv_exp;
-  return r;
 }
+
+MOE_DEVICE float inverse(float s) { return s == 0.f ? 0.f : 1.f / s; }
 
 // FULL: E == LPR * NPL, no column is missing
 template <int LPR, int NPL, bool FULL>
@@ -160,7 +152,9 @@ MOE_DEVICE V block_sum(V v, V* red) {
 constexpr int blocks_per_sm(int npl) { return npl <= 8 ? 4 : npl <= 16 ? 3 : 2; }
 
 // ---------------------------------------------------------------- forward
-// Block b takes chunk b % chunks of sequence b / chunks.  The last block of a
+// Block b takes every chunks-th pass of kStep rows of sequence b / chunks, from
+// pass b % chunks on, so that padding at a sequence's end is spread over its
+// blocks.  The last block of a
 // sequence to finish turns its sums into outputs, and the last sequence's
 // block the sequences' losses into the batch's.  A sequence of one block, and
 // a batch of one sequence, skip the hand-over through global memory.
@@ -168,10 +162,11 @@ template <int LPR, int NPL, int MODE, bool FULL>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(NPL))
 balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restrict__ ids,
                const uint8_t* __restrict__ mask, int L, int E, int K, int n_seq, int chunks,
-               int rows_per_block, int shift, Scratch sc, int32_t* __restrict__ counts,
+               int shift, Scratch sc, int32_t* __restrict__ counts,
                float* __restrict__ mean_prob, int32_t* __restrict__ valid,
                float* __restrict__ losses, int32_t* __restrict__ dev_status) {
   constexpr int RPW = 32 / LPR;
+  constexpr int KPL = 32 / LPR;  // replicas of a token per lane, K <= 32
   constexpr int kStep = kWarps * RPW;
   extern __shared__ float smem[];
   float* psm = smem;                                              // [kWarps][E]
@@ -181,8 +176,7 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
   __shared__ int ired[kWarps];
   __shared__ int bad, last;
   const int seq = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  const int r0 = chunk * rows_per_block;
-  const int r1 = min(L, r0 + rows_per_block);
+  const int stride = chunks * kStep;
   const size_t t0 = (size_t)seq * L;
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
   const int lig = lane % LPR, sub = lane / LPR;
@@ -194,19 +188,13 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
 
   // this row, the next one's logits and the one after's mask are in flight
   const uint8_t* mrow = mask ? mask + t0 : nullptr;
-  auto kept_row = [&](int r) { return r < r1 && (!mrow || __ldg(mrow + r)); };
+  auto kept_row = [&](int r) { return r < L && (!mrow || __ldg(mrow + r)); };
   const float* base = logits + t0 * ld;
-  int r = r0 + warp * RPW + sub;
-  bool on = kept_row(r), on1 = kept_row(r + kStep);
+  const int32_t* idrow = ids + t0 * K;
+  int r = chunk * kStep + warp * RPW + sub;
+  bool on = kept_row(r), on1 = kept_row(r + stride);
   float v[NPL];
   load_row<LPR, NPL, FULL>(base + (size_t)r * ld, E, lig, on, v);
-
-  for (int i = tid; i < (r1 - r0) * K; i += kThreads) {
-    if (mrow && !__ldg(mrow + r0 + i / K)) continue;
-    const int id = __ldg(ids + (t0 + r0) * K + i);
-    if ((unsigned)id < (unsigned)E) atomicAdd(&hist[id], 1);
-    else moe_set_status(dev_status, MOE_DEV_BAD_EXPERT_ID);
-  }
 
   float acc[NPL];
 #pragma unroll
@@ -214,23 +202,55 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
   float z = 0.f;
   int kept = 0;
   bool nan = false;
-  for (int rb = r0 + warp * RPW; rb < r1; rb += kStep) {
-    float nx[NPL], u[NPL];
-    load_row<LPR, NPL, FULL>(base + (size_t)(r + kStep) * ld, E, lig, on1, nx);
-    const bool on2 = kept_row(r + 2 * kStep);
-    const RowSums w = row_probs<LPR, NPL, MODE>(v, u);  // a row left out gives zeros
+  for (int rb = chunk * kStep + warp * RPW; rb < L; rb += stride) {
+    float nx[NPL];
+    load_row<LPR, NPL, FULL>(base + (size_t)(r + stride) * ld, E, lig, on1, nx);
+    const bool on2 = kept_row(r + 2 * stride);
+    if (__any_sync(0xffffffffu, on)) {  // else the warp's rows are padding
+      int id[KPL];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) acc[i] = fmaf(u[i], w.inv, acc[i]);
-    if (on && lig == 0) {
-      z = fmaf(w.lse, w.lse, z);
-      ++kept;
-      nan |= !(w.inv == w.inv);
+      for (int j = 0; j < KPL; ++j) {
+        const int k = lig + LPR * j;
+        id[j] = on && k < K ? __ldg(idrow + (size_t)r * K + k) : 0;
+      }
+      const float m = row_max<LPR, NPL>(v);
+      float u[NPL];
+      float s = 0.f;
+      exp_row(v, m, [&](int i, float e) {
+        s += e;
+        if constexpr (MODE == MOE_SCORE_SOFTMAX_RENORM) u[i] = e;
+      });
+      s = group_sum<LPR>(s);
+      float inv = inverse(s);
+      if constexpr (MODE != MOE_SCORE_SOFTMAX_RENORM) {
+        float q = 0.f;
+        sigmoid_row(v, m, [&](int i, float x) {
+          q += x;
+          u[i] = x;
+        });
+        inv = inverse(group_sum<LPR>(q));
+      }
+      // a row left out is all -inf and adds zeros
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) acc[i] = fmaf(u[i], inv, acc[i]);
+      if (on && lig == 0) {
+        const float lse = s == 0.f ? 0.f : m + logf(s);
+        z = fmaf(lse, lse, z);
+        ++kept;
+        nan |= !(inv == inv);
+      }
+#pragma unroll
+      for (int j = 0; j < KPL; ++j)
+        if (on && lig + LPR * j < K) {
+          if ((unsigned)id[j] < (unsigned)E) atomicAdd(&hist[id[j]], 1);
+          else moe_set_status(dev_status, MOE_DEV_BAD_EXPERT_ID);
+        }
     }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) v[i] = nx[i];
     on = on1;
     on1 = on2;
-    r += kStep;
+    r += stride;
   }
   // the warp's rows, then the block's warps in order
 #pragma unroll
@@ -380,7 +400,7 @@ __host__ __device__ constexpr int buf_stride(int E, int lpr) { return (E + 31) /
 // AUX: with the losses' gradient (reads the whole row of logits).
 template <int LPR, int NPL, int MODE, bool AUX, bool FULL>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(NPL))
-route_backward_kernel(RouteBackwardArgs a, int L, int chunks, int rows_per_block) {
+route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
   constexpr int RPW = 32 / LPR;
   constexpr int KPL = 32 / LPR;  // replicas of a token per lane, K <= 32
   constexpr int kStep = kWarps * RPW;
@@ -393,8 +413,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks, int rows_per_block
   // the row's routing gradient; zero between rows
   float* buf = smem + (AUX ? E : 0) + (size_t)(warp * RPW + sub) * buf_stride(E, LPR);
   const int seq = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  const int r0 = chunk * rows_per_block;
-  const int r1 = min(L, r0 + rows_per_block);
+  const int stride = chunks * kStep;
   const size_t t0 = (size_t)seq * L;
   if (routing)
     for (int c = lig; c < E; c += LPR) buf[c] = 0.f;
@@ -402,10 +421,10 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks, int rows_per_block
   pdl_trigger();
 
   const uint8_t* mrow = a.mask ? a.mask + t0 : nullptr;
-  auto kept_row = [&](int r) { return r < r1 && (!mrow || __ldg(mrow + r)); };
+  auto kept_row = [&](int r) { return r < L && (!mrow || __ldg(mrow + r)); };
   const float* base = a.logits + t0 * a.ld;
-  int r = r0 + warp * RPW + sub;
-  bool on = kept_row(r), on1 = kept_row(r + kStep);
+  int r = chunk * kStep + warp * RPW + sub;
+  bool on = kept_row(r), on1 = kept_row(r + stride);
   float v[NPL];
   if constexpr (AUX) load_row<LPR, NPL, FULL>(base + (size_t)r * a.ld, E, lig, on, v);
 
@@ -423,12 +442,21 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks, int rows_per_block
   const float inv_scale = !kSigmoid ? 1.f : a.scale != 0.f ? 1.f / a.scale : 0.f;
   __syncthreads();
 
-  for (int rb = r0 + warp * RPW; rb < r1; rb += kStep) {
+  for (int rb = chunk * kStep + warp * RPW; rb < L; rb += stride) {
     const size_t t = t0 + r;
-    const bool in = r < r1;
+    const bool in = r < L;
+    float* out = a.dlogits + t * a.ld_d;
     float nx[NPL];
-    if constexpr (AUX) load_row<LPR, NPL, FULL>(base + (size_t)(r + kStep) * a.ld, E, lig, on1, nx);
-    const bool on2 = kept_row(r + 2 * kStep);
+    if constexpr (AUX) load_row<LPR, NPL, FULL>(base + (size_t)(r + stride) * a.ld, E, lig, on1, nx);
+    const bool on2 = kept_row(r + 2 * stride);
+    if (!__any_sync(0xffffffffu, on)) {  // the warp's rows are padding
+      if (in) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+          if (FULL || lig + LPR * i < E) out[lig + LPR * i] = 0.f;
+        if (a.d_shared_gate && lig == 0) out[E] = 0.f;
+      }
+    } else {
     int id[KPL];
     float wk[KPL], gk[KPL];
     if (routing) {
@@ -441,18 +469,51 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks, int rows_per_block
         gk[j] = have ? __ldg(a.d_weights + t * K + k) : 0.f;
       }
     }
-    float u[NPL];
-    RowSums w;
-    float dot = 0.f;
+    // mode 0: e^(v - max); mode 1: the smaller of sigmoid and 1 - sigmoid,
+    // from which both follow without cancellation, or for a row of negative
+    // logits alone the scaled sigmoid
+    float x[NPL];
+    float m = 0.f, lse = 0.f, inv = 0.f, inv_exp = 0.f, dot = 0.f;
+    bool pos = true;
     if constexpr (AUX) {
-      w = row_probs<LPR, NPL, MODE>(v, u);
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const int c = lig + LPR * i;
-        u[i] *= w.inv;
-        if (FULL || c < E) dot = fmaf(smem[c], u[i], dot);
+      m = row_max<LPR, NPL>(v);
+      float s = 0.f;
+      if (!kSigmoid || gz != 0.f) {
+        exp_row(v, m, [&](int i, float e) {
+          s += e;
+          if constexpr (!kSigmoid) x[i] = e;
+        });
+        s = group_sum<LPR>(s);
+        lse = s == 0.f ? 0.f : m + logf(s);
+        inv_exp = inverse(s);
       }
-      dot = group_sum<LPR>(dot);
+      if constexpr (kSigmoid) {
+        pos = m >= 0.f;
+        s = 0.f;
+        if (pos) {
+#pragma unroll
+          for (int i = 0; i < NPL; ++i) {
+            const float e = ex2(-fabsf(v[i]) * kLog2E);
+            x[i] = e * rcp(1.f + e);
+            const float sg = v[i] > 0.f ? 1.f - x[i] : x[i];
+            s += FULL || lig + LPR * i < E ? sg : 0.f;
+            if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], sg, dot);
+          }
+        } else {
+          sigmoid_row(v, m, [&](int i, float u) {
+            x[i] = u;
+            s += u;
+            if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], u, dot);
+          });
+        }
+        inv = inverse(group_sum<LPR>(s));
+      } else {
+        inv = inv_exp;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+          if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], x[i], dot);
+      }
+      dot = group_sum<LPR>(dot) * inv;
     }
     if (routing) {
       float wg = 0.f;
@@ -497,20 +558,24 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks, int rows_per_block
       }
       __syncwarp();
     }
-    const float zl = gz * w.lse, zm = w.inv_exp;
-    float* out = a.dlogits + t * a.ld_d;
+    // p (a - dot) = x (a inv - dot inv); in mode 0 the z-loss's p zl joins it
+    const float zl = gz != 0.f ? gz * lse : 0.f;
+    const float shift = kSigmoid ? -dot * inv : (zl - dot) * inv;
+    const float zq = zl * inv_exp;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       const int c = lig + LPR * i;
       if (!FULL && c >= E) continue;
       float d = routing ? buf[c] : 0.f;
       if constexpr (AUX && !kSigmoid) {
-        float g = smem[c] - dot;
-        if (gz != 0.f) g += zl;
-        d = fmaf(u[i], g, d);
+        d = fmaf(x[i], fmaf(smem[c], inv, shift), d);
       } else if constexpr (AUX) {
-        d = fmaf(u[i], smem[c] - dot, d) * sigmoid_tail(v[i]);
-        if (gz != 0.f) d = fmaf(zl, exp_fast(v[i] - w.max) * zm, d);
+        const float other = 1.f - x[i];
+        const bool up = v[i] > 0.f;
+        const float sg = pos && up ? other : x[i];
+        const float tail = !pos ? rcp(1.f + ex2(v[i] * kLog2E)) : up ? x[i] : other;
+        d = fmaf(sg, fmaf(smem[c], inv, shift), d) * tail;
+        if (gz != 0.f) d = fmaf(zq, ex2((v[i] - m) * kLog2E), d);
       }
       if (in) out[c] = on ? d : 0.f;
     }
@@ -531,13 +596,14 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks, int rows_per_block
       }
       out[E] = g;
     }
+    }
     if constexpr (AUX) {
 #pragma unroll
       for (int i = 0; i < NPL; ++i) v[i] = nx[i];
     }
     on = on1;
     on1 = on2;
-    r += kStep;
+    r += stride;
   }
 }
 
@@ -562,17 +628,11 @@ Shape shape_of(int E) {
 // warps each; a fixed SM count, so that the scratch size does not depend on
 // which device is current.
 constexpr int kGridSms = 152;
-struct Chunks {
-  int chunks, rows;
-};
-Chunks chunks_of(int L, int n_seq, int E) {
+int chunks_of(int L, int n_seq, int E) {
   const Shape sh = shape_of(E);
-  const int pass = kWarps * (32 / sh.lpr);
-  const int most = moe_cdiv(blocks_per_sm(sh.npl) * kGridSms, n_seq);
-  Chunks c;
-  c.rows = moe_cdiv(moe_cdiv(L, most), pass) * pass;
-  c.chunks = moe_cdiv(L, c.rows);
-  return c;
+  const int passes = moe_cdiv(L, kWarps * (32 / sh.lpr));
+  const int wave = blocks_per_sm(sh.npl) * kGridSms / n_seq;
+  return passes < wave ? passes : wave > 0 ? wave : 1;
 }
 
 Scratch scratch_of(void* p, int E, int n_seq, int blocks, size_t* bytes) {
@@ -625,8 +685,8 @@ struct BalanceArgs {
 template <int LPR, int NPL, bool FULL>
 cudaError_t run_balance(const BalanceArgs& a, cudaStream_t stream) {
   const int L = a.T / a.n_seq;
-  const Chunks c = chunks_of(L, a.n_seq, a.E);
-  const Scratch s = scratch_of(a.scratch, a.E, a.n_seq, a.n_seq * c.chunks, nullptr);
+  const int chunks = chunks_of(L, a.n_seq, a.E);
+  const Scratch s = scratch_of(a.scratch, a.E, a.n_seq, a.n_seq * chunks, nullptr);
   // L probabilities of at most 1 sum to at most 2^bits, so 2^61 in fixed point
   int bits = 0;
   while (bits < 31 && (1ll << bits) < L) ++bits;
@@ -634,15 +694,15 @@ cudaError_t run_balance(const BalanceArgs& a, cudaStream_t stream) {
   auto k = a.mode == MOE_SCORE_SOFTMAX_RENORM
                ? balance_kernel<LPR, NPL, MOE_SCORE_SOFTMAX_RENORM, FULL>
                : balance_kernel<LPR, NPL, MOE_SCORE_SIGMOID_BIAS_SCALED, FULL>;
-  return moe_launch(k, dim3(a.n_seq * c.chunks), dim3(kThreads), smem, stream, 1, a.logits, a.ld,
-                    a.ids, a.mask, L, a.E, a.K, a.n_seq, c.chunks, c.rows, 61 - bits, s, a.counts,
+  return moe_launch(k, dim3(a.n_seq * chunks), dim3(kThreads), smem, stream, 1, a.logits, a.ld,
+                    a.ids, a.mask, L, a.E, a.K, a.n_seq, chunks, 61 - bits, s, a.counts,
                     a.mean_prob, a.valid, a.losses, a.dev_status);
 }
 
 template <int LPR, int NPL, bool FULL>
 cudaError_t run_route_backward(const RouteBackwardArgs& a, cudaStream_t stream) {
   const int L = a.T / a.n_seq;
-  const Chunks c = chunks_of(L, a.n_seq, a.E);
+  const int chunks = chunks_of(L, a.n_seq, a.E);
   const bool aux = a.grad_losses != nullptr;
   const size_t smem =
       4 * ((aux ? a.E : 0) +
@@ -652,15 +712,14 @@ cudaError_t run_route_backward(const RouteBackwardArgs& a, cudaStream_t stream) 
                                : route_backward_kernel<LPR, NPL, S0, false, false>)
                         : (aux ? route_backward_kernel<LPR, NPL, S1, true, FULL>
                                : route_backward_kernel<LPR, NPL, S1, false, false>);
-  return moe_launch(k, dim3(a.n_seq * c.chunks), dim3(kThreads), smem, stream, 1, a, L, c.chunks,
-                    c.rows);
+  return moe_launch(k, dim3(a.n_seq * chunks), dim3(kThreads), smem, stream, 1, a, L, chunks);
 }
 
 }  // namespace
 
 size_t balance_loss_scratch_bytes(int T, int E, int n_seq) {
   const int L = T / n_seq;
-  const int chunks = L > 0 ? chunks_of(L, n_seq, E).chunks : 1;
+  const int chunks = L > 0 ? chunks_of(L, n_seq, E) : 1;
   size_t bytes = 0;
   scratch_of(nullptr, E, n_seq, n_seq * chunks, &bytes);
   return bytes;
