@@ -18,10 +18,13 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 #include "sm100_ptx.cuh"
 
 namespace {
+
+using namespace moe_f32x2;
 
 constexpr int kMaxWarps = 16;
 
@@ -185,25 +188,6 @@ add_rmsnorm_kernel(const uint4* x, const uint4* residual, const void* __restrict
   }
 }
 
-// two fp32 products (and additions) in one instruction
-MOE_DEVICE float2 mul2(float2 a, float2 b) {
-  unsigned long long d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)),
-        "l"(*reinterpret_cast<unsigned long long*>(&b)));
-  return *reinterpret_cast<float2*>(&d);
-}
-MOE_DEVICE float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)),
-        "l"(*reinterpret_cast<unsigned long long*>(&b)),
-        "l"(*reinterpret_cast<unsigned long long*>(&c)));
-  return *reinterpret_cast<float2*>(&d);
-}
-MOE_DEVICE float2 pair(float a) { return make_float2(a, a); }
 MOE_DEVICE void unpack4(const uint4& v, float2* f) {
   f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
   f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));

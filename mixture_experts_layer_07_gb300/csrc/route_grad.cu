@@ -24,9 +24,12 @@
 // Determinism: a block's probability sums are fp32 in a fixed order; across
 // blocks they are added as 64-bit fixed point, so the order does not matter.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 
 namespace {
+
+using namespace moe_f32x2;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
@@ -36,7 +39,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 struct Scratch {
   unsigned long long* psum;  // [n_seq][E] fixed-point sums
   int32_t* cnt;              // [n_seq][E]
-  uint32_t* head;            // [n_seq][4]: kept tokens, any NaN, blocks done, unused
+  unsigned long long* head;  // [n_seq]: blocks done << 48 | blocks with a NaN << 32 | kept tokens
   uint32_t* done;            // sequences done
   float* zpart;              // [blocks] sums of lse^2
   float* bal_seq;            // [n_seq]
@@ -58,8 +61,8 @@ MOE_DEVICE float group_max(float v) {
 
 constexpr float kLog2E = 1.4426950408889634f;
 
-// Hardware 2^x (relative error about 2^-22; results below 2^-126 are 0) and,
-// for 1 <= x <= 2, 1 / x.
+// Hardware 2^x (relative error about 2^-22; results below 2^-126 are 0) and
+// 1 / x (about 2^-23).
 MOE_DEVICE float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -77,21 +80,29 @@ MOE_DEVICE float sigmoid_tail(float l) {
   return (l > 0.f ? a : 1.f) * rcp(1.f + a);
 }
 
-// f(i, e^(v[i] - m)) for every column.  Folding m into one multiply-add rounds
-// m log2(e) once, a factor that all columns share: it cancels in a ratio and
-// shifts the sum's logarithm by at most |m| 2^-24.  Maxima past 10^4 -- rows of
-// the type's lowest value among them, where the folded product overflows --
-// take the difference first.
-template <int NPL, typename F>
-MOE_DEVICE void exp_row(const float (&v)[NPL], float m, F&& f) {
-  if (fabsf(m) <= 1e4f) {
-    const float ml = m * kLog2E;
+// The lane's sum of e^(v[i] - m), which STORE leaves in v.  Folding m into one
+// multiply-add rounds m log2(e) once, a factor that all columns share: it
+// cancels in a ratio and shifts the sum's logarithm by at most |m| 2^-24.
+// Maxima past 10^4 -- rows of the type's lowest value among them, where the
+// folded product overflows -- take the difference first.
+template <bool STORE, int NPL>
+MOE_DEVICE float exp_row(float (&v)[NPL], float m) {
+  float2 s = pair(0.f);
+  const bool fold = fabsf(m) <= 1e4f;
+  const float2 ml = pair(-m * kLog2E);
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) f(i, ex2(fmaf(v[i], kLog2E, -ml)));
-  } else {
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) f(i, ex2((v[i] - m) * kLog2E));
+  for (int i = 0; i < NPL; i += 2) {
+    float2 x = make_float2(v[i], v[i + 1]);
+    if (fold) x = fma2(x, pair(kLog2E), ml);
+    else x = make_float2((x.x - m) * kLog2E, (x.y - m) * kLog2E);
+    x = make_float2(ex2(x.x), ex2(x.y));
+    s = add2(s, x);
+    if constexpr (STORE) {
+      v[i] = x.x;
+      v[i + 1] = x.y;
+    }
   }
+  return s.x + s.y;
 }
 
 // The row's maximum, 0 where that is -inf (no expert is left).
@@ -104,52 +115,77 @@ MOE_DEVICE float row_max(const float (&v)[NPL]) {
   return m == kNegInf ? 0.f : m;
 }
 
-// Mode 1: f(i, u) with u = sigmoid(v[i]) e^c, c = max(0, -m): the common
-// factor cancels in u / sum u and keeps rows of very negative logits from
-// vanishing.
-template <int NPL, typename F>
-MOE_DEVICE void sigmoid_row(const float (&v)[NPL], float m, F&& f) {
+// Mode 1: v[i] <- sigmoid(v[i]) e^c with c = max(0, -m), the common factor
+// cancels in a ratio and keeps rows of very negative logits from vanishing;
+// returns the sum over the lane's columns.
+template <int NPL>
+MOE_DEVICE float sigmoid_row(float (&v)[NPL], float m) {
+  float s = 0.f;
   if (m >= 0.f) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       const float a = ex2(-fabsf(v[i]) * kLog2E);
-      f(i, (v[i] > 0.f ? 1.f : a) * rcp(1.f + a));
+      v[i] = (v[i] > 0.f ? 1.f : a) * rcp(1.f + a);
+      s += v[i];
     }
   } else {  // every logit is negative
 #pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      f(i, ex2((v[i] - m) * kLog2E) * rcp(1.f + ex2(v[i] * kLog2E)));
+    for (int i = 0; i < NPL; ++i) {
+      v[i] = ex2((v[i] - m) * kLog2E) * rcp(1.f + ex2(v[i] * kLog2E));
+      s += v[i];
+    }
   }
+  return s;
 }
 
-MOE_DEVICE float inverse(float s) { return s == 0.f ? 0.f : 1.f / s; }
+// 1 / s, 0 for an empty row's sum
+MOE_DEVICE float inverse(float s) { return s == 0.f ? 0.f : rcp(s); }
 
-// FULL: E == LPR * NPL, no column is missing
+// A row's columns lig + LPR*i, -inf past E and where the row is not `on`.
+// FULL: E == LPR * NPL, no column is missing.
 template <int LPR, int NPL, bool FULL>
 MOE_DEVICE void load_row(const float* __restrict__ row, int E, int lig, bool on, float (&v)[NPL]) {
+  if (on) {
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int c = lig + LPR * i;
-    v[i] = on && (FULL || c < E) ? __ldg(row + c) : kNegInf;
+    for (int i = 0; i < NPL; ++i)
+      v[i] = FULL || lig + LPR * i < E ? __ldg(row + lig + LPR * i) : kNegInf;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = kNegInf;
   }
 }
 
-template <typename V>
-MOE_DEVICE V block_sum(V v, V* red) {
+// Sums of a pair over the block; `red` is free again after the next barrier.
+template <typename A, typename B>
+struct Pair {
+  A a;
+  B b;
+};
+template <typename A, typename B>
+MOE_DEVICE void block_sums(Pair<A, B>* red, A& a, B& b) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if (lane_id() == 0) red[warp_id()] = {a, b};
   __syncthreads();
-  if (lane_id() == 0) red[warp_id()] = v;
-  __syncthreads();
-  v = red[0];
+  a = red[0].a;
+  b = red[0].b;
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) v += red[w];
-  return v;
+  for (int w = 1; w < kWarps; ++w) {
+    a += red[w].a;
+    b += red[w].b;
+  }
 }
 
 // Blocks per SM that the registers of a row pair (this row and the next one,
-// loaded ahead) allow; the grid is that many per SM.
+// loaded ahead) allow; the grid is that many per SM.  The gradient holds a
+// third row, and with few lanes per row several replicas per lane.
 constexpr int blocks_per_sm(int npl) { return npl <= 8 ? 4 : npl <= 16 ? 3 : 2; }
+constexpr int back_blocks_per_sm(int lpr, int npl) {
+  return npl <= 4 ? 4 : npl <= 8 ? 3 : npl <= 16 && lpr > 8 ? 3 : 2;
+}
 
 // ---------------------------------------------------------------- forward
 // Block b takes every chunks-th pass of kStep rows of sequence b / chunks, from
@@ -171,10 +207,11 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
   extern __shared__ float smem[];
   float* psm = smem;                                              // [kWarps][E]
   int32_t* hist = reinterpret_cast<int32_t*>(smem + kWarps * E);  // [E]
-  __shared__ float fred[kWarps];
-  __shared__ double dred[kWarps];
-  __shared__ int ired[kWarps];
+  __shared__ Pair<float, int> fired[kWarps];
+  __shared__ Pair<float, float> ffred[kWarps];
+  __shared__ Pair<int, int> iired[kWarps];
   __shared__ int bad, last;
+  __shared__ unsigned long long total_s;
   const int seq = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
   const int stride = chunks * kStep;
   const size_t t0 = (size_t)seq * L;
@@ -186,72 +223,82 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
   pdl_trigger();
   __syncthreads();
 
-  // this row, the next one's logits and the one after's mask are in flight
+  // this row, the next one's logits and ids and the one after's mask are in
+  // flight
   const uint8_t* mrow = mask ? mask + t0 : nullptr;
   auto kept_row = [&](int r) { return r < L && (!mrow || __ldg(mrow + r)); };
-  const float* base = logits + t0 * ld;
-  const int32_t* idrow = ids + t0 * K;
-  int r = chunk * kStep + warp * RPW + sub;
+  auto load = [&](int r, bool on, float(&v)[NPL], int(&id)[KPL]) {
+    load_row<LPR, NPL, FULL>(logits + (t0 + r) * ld, E, lig, on, v);
+#pragma unroll
+    for (int j = 0; j < KPL; ++j)
+      id[j] = on && lig + LPR * j < K ? __ldg(ids + (t0 + r) * K + lig + LPR * j) : 0;
+  };
+  const int rw = chunk * kStep + warp * RPW;
+  int r = rw + sub;
   bool on = kept_row(r), on1 = kept_row(r + stride);
-  float v[NPL];
-  load_row<LPR, NPL, FULL>(base + (size_t)r * ld, E, lig, on, v);
 
   float acc[NPL];
 #pragma unroll
   for (int i = 0; i < NPL; ++i) acc[i] = 0.f;
-  float z = 0.f;
-  int kept = 0;
+  float z = 0.f, keep_m = 0.f, keep_s = 0.f;
+  int kept = 0, it = 0;
   bool nan = false;
-  for (int rb = chunk * kStep + warp * RPW; rb < L; rb += stride) {
-    float nx[NPL];
-    load_row<LPR, NPL, FULL>(base + (size_t)(r + stride) * ld, E, lig, on1, nx);
+  // the logarithms of LPR rows at a time, one per lane of the row's group
+  auto add_z = [&]() {
+    const float lse = keep_s == 0.f ? 0.f : keep_m + logf(keep_s);
+    z = fmaf(lse, lse, z);
+    keep_s = 0.f;
+  };
+  auto row_step = [&](float(&v)[NPL], int(&id)[KPL], float(&nx)[NPL], int(&idn)[KPL]) {
+    load(r + stride, on1, nx, idn);
     const bool on2 = kept_row(r + 2 * stride);
     if (__any_sync(0xffffffffu, on)) {  // else the warp's rows are padding
-      int id[KPL];
-#pragma unroll
-      for (int j = 0; j < KPL; ++j) {
-        const int k = lig + LPR * j;
-        id[j] = on && k < K ? __ldg(idrow + (size_t)r * K + k) : 0;
-      }
       const float m = row_max<LPR, NPL>(v);
-      float u[NPL];
-      float s = 0.f;
-      exp_row(v, m, [&](int i, float e) {
-        s += e;
-        if constexpr (MODE == MOE_SCORE_SOFTMAX_RENORM) u[i] = e;
-      });
-      s = group_sum<LPR>(s);
-      float inv = inverse(s);
-      if constexpr (MODE != MOE_SCORE_SOFTMAX_RENORM) {
-        float q = 0.f;
-        sigmoid_row(v, m, [&](int i, float x) {
-          q += x;
-          u[i] = x;
-        });
-        inv = inverse(group_sum<LPR>(q));
+      float s, inv;
+      if constexpr (MODE == MOE_SCORE_SOFTMAX_RENORM) {
+        s = group_sum<LPR>(exp_row<true>(v, m));
+        inv = inverse(s);
+      } else {
+        s = group_sum<LPR>(exp_row<false>(v, m));
+        inv = inverse(group_sum<LPR>(sigmoid_row(v, m)));
       }
       // a row left out is all -inf and adds zeros
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) acc[i] = fmaf(u[i], inv, acc[i]);
-      if (on && lig == 0) {
-        const float lse = s == 0.f ? 0.f : m + logf(s);
-        z = fmaf(lse, lse, z);
-        ++kept;
-        nan |= !(inv == inv);
+      for (int i = 0; i < NPL; i += 2) {
+        const float2 x = fma2(make_float2(v[i], v[i + 1]), pair(inv), make_float2(acc[i], acc[i + 1]));
+        acc[i] = x.x;
+        acc[i + 1] = x.y;
       }
-#pragma unroll
-      for (int j = 0; j < KPL; ++j)
-        if (on && lig + LPR * j < K) {
-          if ((unsigned)id[j] < (unsigned)E) atomicAdd(&hist[id[j]], 1);
-          else moe_set_status(dev_status, MOE_DEV_BAD_EXPERT_ID);
+      if (on) {
+        if (lig == it % LPR) {
+          keep_m = m;
+          keep_s = s;
+          ++kept;
         }
-    }
+        nan |= !(inv == inv);
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) v[i] = nx[i];
+        for (int j = 0; j < KPL; ++j)
+          if (lig + LPR * j < K) {
+            if ((unsigned)id[j] < (unsigned)E) atomicAdd(&hist[id[j]], 1);
+            else moe_set_status(dev_status, MOE_DEV_BAD_EXPERT_ID);
+          }
+      }
+    }
+    if (++it % LPR == 0) add_z();
     on = on1;
     on1 = on2;
     r += stride;
+  };
+  float va[NPL], vb[NPL];
+  int ia[KPL], ib[KPL];
+  load(r, on, va, ia);
+  for (int rb = rw; rb < L;) {
+    row_step(va, ia, vb, ib);
+    if ((rb += stride) >= L) break;
+    row_step(vb, ib, va, ia);
+    rb += stride;
   }
+  add_z();
   // the warp's rows, then the block's warps in order
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
@@ -262,8 +309,8 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
     if (sub == 0 && (FULL || c < E)) psm[warp * E + c] = s;
   }
   if (nan) bad = 1;
-  z = block_sum(z, fred);
-  int nv = block_sum(kept, ired);  // its barriers also publish psm, hist and bad
+  int nv = kept;
+  block_sums(fired, z, nv);  // its barrier also publishes psm, hist and bad
   bool poisoned = bad;
   auto block_prob = [&](int e) {
     float s = 0.f;
@@ -272,7 +319,7 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
     return s;
   };
 
-  uint32_t* head = sc.head + (size_t)seq * 4;
+  unsigned long long* head = sc.head + seq;
   if (chunks > 1) {
     const float fix = __int_as_float((shift + 127) << 23);  // 2^shift
     for (int e = tid; e < E; e += kThreads) {
@@ -281,60 +328,78 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
         atomicAdd(sc.psum + (size_t)seq * E + e, (unsigned long long)__float2ll_rn(s * fix));
       if (hist[e]) atomicAdd(sc.cnt + (size_t)seq * E + e, hist[e]);
     }
-    if (tid == 0) {
-      sc.zpart[blockIdx.x] = z;
-      atomicAdd(head, (uint32_t)nv);
-      if (poisoned) atomicOr(head + 1, 1u);
+    if (tid == 0) sc.zpart[blockIdx.x] = z;
+    __syncthreads();
+    if (tid == 0) {  // fences of one thread order the whole block's work, by the barriers
+      const unsigned long long mine =
+          1ull << 48 | (unsigned long long)poisoned << 32 | (unsigned)nv;
+      __threadfence();
+      total_s = atomicAdd(head, mine) + mine;
+      __threadfence();
     }
-    __threadfence();
     __syncthreads();
-    if (tid == 0) last = atomicAdd(head + 2, 1u) == (uint32_t)(chunks - 1);
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    nv = (int)__ldcg(head);
-    poisoned = __ldcg(head + 1) != 0;
+    if (total_s >> 48 != (unsigned)chunks) return;
+    nv = (int)(uint32_t)total_s;
+    poisoned = (total_s >> 32 & 0xffff) != 0;
   }
 
   // last block of the sequence: its outputs and its share of the losses
   const float poison = poisoned ? __int_as_float(0x7fffffff) : 0.f;
   const float inv_n = nv ? 1.f / (float)nv : 0.f;
-  const float unfix = __int_as_float((127 - shift) << 23);  // 2^-shift
   float part = 0.f;
-  for (int e = tid; e < E; e += kThreads) {
-    const size_t o = (size_t)seq * E + e;
-    int c;
-    float p;
-    if (chunks > 1) {
-      c = __ldcg(sc.cnt + o);
-      p = __ull2float_rn(__ldcg(sc.psum + o)) * unfix * inv_n;
+  if (chunks > 1) {
+    constexpr int kPer = (LPR * NPL + kThreads - 1) / kThreads;  // experts per thread
+    constexpr int kZ = 3;                                        // blocks per thread, as a rule
+    unsigned long long ps[kPer];
+    int c[kPer];
+    float zp[kZ];
+    float* zrow = sc.zpart + (size_t)seq * chunks;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid + i * kThreads;
+      const size_t o = (size_t)seq * E + e;
+      ps[i] = e < E ? __ldcg(sc.psum + o) : 0ull;
+      c[i] = e < E ? __ldcg(sc.cnt + o) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kZ; ++i) zp[i] = tid + i * kThreads < chunks ? __ldcg(zrow + tid + i * kThreads) : 0.f;
+    const float unfix = __int_as_float((127 - shift) << 23);  // 2^-shift
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid + i * kThreads;
+      if (e >= E) continue;
+      const size_t o = (size_t)seq * E + e;
+      const float p = __ull2float_rn(ps[i]) * unfix * inv_n;
+      counts[o] = c[i];
+      mean_prob[o] = p + poison;
+      part = fmaf((float)c[i], p, part);
       sc.cnt[o] = 0;
       sc.psum[o] = 0;
-    } else {
-      c = hist[e];
-      p = block_prob(e) * inv_n;
     }
-    counts[o] = c;
-    mean_prob[o] = p + poison;
-    part = fmaf((float)c, p, part);
-  }
-  if (chunks > 1) {
     z = 0.f;
-    for (int i = tid; i < chunks; i += kThreads) {
-      float* zp = sc.zpart + (size_t)seq * chunks + i;
-      z += __ldcg(zp);
-      *zp = 0.f;
+#pragma unroll
+    for (int i = 0; i < kZ; ++i) z += zp[i];
+    for (int i = tid + kZ * kThreads; i < chunks; i += kThreads) z += __ldcg(zrow + i);
+    for (int i = tid; i < chunks; i += kThreads) zrow[i] = 0.f;
+  } else {
+    for (int e = tid; e < E; e += kThreads) {
+      const size_t o = (size_t)seq * E + e;
+      const float p = block_prob(e) * inv_n;
+      counts[o] = hist[e];
+      mean_prob[o] = p + poison;
+      part = fmaf((float)hist[e], p, part);
     }
-    z = block_sum(z, fred);
   }
-  const float bal = block_sum(part, fred) * ((float)E / (float)K) * inv_n + poison;
+  if (chunks == 1 && tid != 0) z = 0.f;  // the block's sum already
+  block_sums(ffred, part, z);
+  const float bal = part * ((float)E / (float)K) * inv_n + poison;
   if (n_seq == 1) {
     if (tid == 0) {
       losses[0] = bal;
       losses[1] = z * inv_n;
       valid[0] = valid[1] = nv;
       valid[2] = nv > 0;
-      if (chunks > 1) head[0] = head[1] = head[2] = 0;
+      if (chunks > 1) *head = 0;
     }
     return;
   }
@@ -342,32 +407,31 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
     sc.bal_seq[seq] = bal;
     sc.z_seq[seq] = z;
     valid[seq] = nv;
-    if (chunks > 1) head[0] = head[1] = head[2] = 0;
+    if (chunks > 1) *head = 0;
     __threadfence();
     last = atomicAdd(sc.done, 1u) == (uint32_t)(n_seq - 1);
+    __threadfence();
   }
   __syncthreads();
   if (!last) return;
 
   // last sequence of all: the two losses
-  __threadfence();
-  double b = 0.0, zz = 0.0;
+  float b = 0.f, zz = 0.f;
   int total = 0, full = 0;
   for (int s = tid; s < n_seq; s += kThreads) {
     const int n = __ldcg(valid + s);
-    b += (double)__ldcg(sc.bal_seq + s);
-    zz += (double)__ldcg(sc.z_seq + s);
+    b += __ldcg(sc.bal_seq + s);
+    zz += __ldcg(sc.z_seq + s);
     total += n;
     full += n > 0;
     sc.bal_seq[s] = sc.z_seq[s] = 0.f;
   }
-  b = block_sum(b, dred);
-  zz = block_sum(zz, dred);
-  total = block_sum(total, ired);
-  full = block_sum(full, ired);
+  __syncthreads();
+  block_sums(ffred, b, zz);
+  block_sums(iired, total, full);
   if (tid == 0) {
-    losses[0] = full > 0 ? (float)b / (float)full : 0.f;
-    losses[1] = total > 0 ? (float)zz / (float)total : 0.f;
+    losses[0] = full > 0 ? b / (float)full : 0.f;
+    losses[1] = total > 0 ? zz / (float)total : 0.f;
     valid[n_seq] = total;
     valid[n_seq + 1] = full;
     *sc.done = 0;
@@ -399,7 +463,7 @@ __host__ __device__ constexpr int buf_stride(int E, int lpr) { return (E + 31) /
 
 // AUX: with the losses' gradient (reads the whole row of logits).
 template <int LPR, int NPL, int MODE, bool AUX, bool FULL>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(NPL))
+__global__ void __launch_bounds__(kThreads, back_blocks_per_sm(LPR, NPL))
 route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
   constexpr int RPW = 32 / LPR;
   constexpr int KPL = 32 / LPR;  // replicas of a token per lane, K <= 32
@@ -410,7 +474,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
   const int warp = warp_id(), lane = lane_id();
   const int lig = lane % LPR, sub = lane / LPR;
   const bool routing = a.d_weights != nullptr;
-  // the row's routing gradient; zero between rows
+  // a_e of this sequence (AUX), then the row's routing gradient, zero between rows
   float* buf = smem + (AUX ? E : 0) + (size_t)(warp * RPW + sub) * buf_stride(E, LPR);
   const int seq = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
   const int stride = chunks * kStep;
@@ -422,14 +486,14 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
 
   const uint8_t* mrow = a.mask ? a.mask + t0 : nullptr;
   auto kept_row = [&](int r) { return r < L && (!mrow || __ldg(mrow + r)); };
-  const float* base = a.logits + t0 * a.ld;
-  int r = chunk * kStep + warp * RPW + sub;
+  const int rw = chunk * kStep + warp * RPW;
+  int r = rw + sub;
   bool on = kept_row(r), on1 = kept_row(r + stride);
-  float v[NPL];
-  if constexpr (AUX) load_row<LPR, NPL, FULL>(base + (size_t)r * a.ld, E, lig, on, v);
+  float va[NPL], vb[NPL];
+  if constexpr (AUX) load_row<LPR, NPL, FULL>(a.logits + (t0 + r) * a.ld, E, lig, on, va);
 
   float gz = 0.f;
-  if constexpr (AUX) {  // a_e of this sequence, shared by its rows
+  if constexpr (AUX) {
     const int nv = __ldg(a.valid + seq), total = __ldg(a.valid + a.n_seq),
               full = __ldg(a.valid + a.n_seq + 1);
     gz = total > 0 ? 2.f * __ldg(a.grad_losses + 1) / (float)total : 0.f;
@@ -442,28 +506,32 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
   const float inv_scale = !kSigmoid ? 1.f : a.scale != 0.f ? 1.f / a.scale : 0.f;
   __syncthreads();
 
-  for (int rb = chunk * kStep + warp * RPW; rb < L; rb += stride) {
-    const size_t t = t0 + r;
-    const bool in = r < L;
-    float* out = a.dlogits + t * a.ld_d;
-    float nx[NPL];
-    if constexpr (AUX) load_row<LPR, NPL, FULL>(base + (size_t)(r + stride) * a.ld, E, lig, on1, nx);
+  auto row_step = [&](float(&v)[NPL], float(&nx)[NPL]) {
+    if constexpr (AUX)
+      load_row<LPR, NPL, FULL>(a.logits + (t0 + r + stride) * a.ld, E, lig, on1, nx);
     const bool on2 = kept_row(r + 2 * stride);
-    if (!__any_sync(0xffffffffu, on)) {  // the warp's rows are padding
+    const size_t t = t0 + r;
+    const bool in = r < L, now = on;
+    float* out = a.dlogits + t * a.ld_d;
+    on = on1;
+    on1 = on2;
+    r += stride;
+    if (!__any_sync(0xffffffffu, now)) {  // the warp's rows are padding
       if (in) {
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
           if (FULL || lig + LPR * i < E) out[lig + LPR * i] = 0.f;
         if (a.d_shared_gate && lig == 0) out[E] = 0.f;
       }
-    } else {
+      return;
+    }
     int id[KPL];
     float wk[KPL], gk[KPL];
     if (routing) {
 #pragma unroll
       for (int j = 0; j < KPL; ++j) {
         const int k = lig + LPR * j;
-        const bool have = on && k < K;
+        const bool have = now && k < K;
         id[j] = have ? __ldg(a.ids + t * K + k) : -1;
         wk[j] = have ? __ldg(a.weights + t * K + k) : 0.f;
         gk[j] = have ? __ldg(a.d_weights + t * K + k) : 0.f;
@@ -477,34 +545,34 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
     bool pos = true;
     if constexpr (AUX) {
       m = row_max<LPR, NPL>(v);
-      float s = 0.f;
+      if constexpr (!kSigmoid) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) x[i] = v[i];
+      }
       if (!kSigmoid || gz != 0.f) {
-        exp_row(v, m, [&](int i, float e) {
-          s += e;
-          if constexpr (!kSigmoid) x[i] = e;
-        });
-        s = group_sum<LPR>(s);
+        const float s = group_sum<LPR>(kSigmoid ? exp_row<false>(v, m) : exp_row<true>(x, m));
         lse = s == 0.f ? 0.f : m + logf(s);
         inv_exp = inverse(s);
       }
       if constexpr (kSigmoid) {
         pos = m >= 0.f;
-        s = 0.f;
+        float s = 0.f;
         if (pos) {
 #pragma unroll
           for (int i = 0; i < NPL; ++i) {
             const float e = ex2(-fabsf(v[i]) * kLog2E);
             x[i] = e * rcp(1.f + e);
             const float sg = v[i] > 0.f ? 1.f - x[i] : x[i];
-            s += FULL || lig + LPR * i < E ? sg : 0.f;
+            s += sg;
             if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], sg, dot);
           }
         } else {
-          sigmoid_row(v, m, [&](int i, float u) {
-            x[i] = u;
-            s += u;
-            if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], u, dot);
-          });
+#pragma unroll
+          for (int i = 0; i < NPL; ++i) x[i] = v[i];
+          s = sigmoid_row(x, m);
+#pragma unroll
+          for (int i = 0; i < NPL; ++i)
+            if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], x[i], dot);
         }
         inv = inverse(group_sum<LPR>(s));
       } else {
@@ -521,7 +589,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       int* tag = reinterpret_cast<int*>(buf);
 #pragma unroll
       for (int j = 0; j < KPL; ++j) {
-        if (on && lig + LPR * j < K && (unsigned)id[j] >= (unsigned)E) {
+        if (now && lig + LPR * j < K && (unsigned)id[j] >= (unsigned)E) {
           moe_set_status(a.dev_status, MOE_DEV_BAD_EXPERT_ID);
           id[j] = -1;
         }
@@ -533,10 +601,9 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
 #pragma unroll
       for (int j = 0; j < KPL; ++j) {
         gk[j] = wk[j] * (gk[j] - wg);
-        if (id[j] >= 0) {
-          lost |= tag[id[j]] != lig + LPR * j + 1;
-          if constexpr (kSigmoid && !AUX) gk[j] *= sigmoid_tail(__ldg(base + (size_t)r * a.ld + id[j]));
-        }
+        if (id[j] < 0) continue;
+        lost |= tag[id[j]] != lig + LPR * j + 1;
+        if constexpr (kSigmoid && !AUX) gk[j] *= sigmoid_tail(__ldg(a.logits + t * a.ld + id[j]));
       }
       // top-K gives distinct ids: every replica found its own tag and the
       // values go out together; a repeated id adds up in k order instead
@@ -577,7 +644,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
         d = fmaf(sg, fmaf(smem[c], inv, shift), d) * tail;
         if (gz != 0.f) d = fmaf(zq, ex2((v[i] - m) * kLog2E), d);
       }
-      if (in) out[c] = on ? d : 0.f;
+      if (in) out[c] = now ? d : 0.f;
     }
     if (routing) {
       __syncwarp();
@@ -588,22 +655,20 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
     }
     if (a.d_shared_gate && in && lig == 0) {
       float g = 0.f;
-      if (on) {
-        const float l = __ldg(base + (size_t)r * a.ld + E);
+      if (now) {
+        const float l = __ldg(a.logits + t * a.ld + E);
         const float ea = expf(-fabsf(l));
         const float q = 1.f / (1.f + ea);
         g = __ldg(a.d_shared_gate + t) * (ea * q * q);
       }
       out[E] = g;
     }
-    }
-    if constexpr (AUX) {
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) v[i] = nx[i];
-    }
-    on = on1;
-    on1 = on2;
-    r += stride;
+  };
+  for (int rb = rw; rb < L;) {
+    row_step(va, vb);
+    if ((rb += stride) >= L) break;
+    row_step(vb, va);
+    rb += stride;
   }
 }
 
@@ -628,10 +693,9 @@ Shape shape_of(int E) {
 // warps each; a fixed SM count, so that the scratch size does not depend on
 // which device is current.
 constexpr int kGridSms = 152;
-int chunks_of(int L, int n_seq, int E) {
-  const Shape sh = shape_of(E);
-  const int passes = moe_cdiv(L, kWarps * (32 / sh.lpr));
-  const int wave = blocks_per_sm(sh.npl) * kGridSms / n_seq;
+int chunks_of(int L, int n_seq, int lpr, int blocks) {
+  const int passes = moe_cdiv(L, kWarps * (32 / lpr));
+  const int wave = blocks * kGridSms / n_seq;
   return passes < wave ? passes : wave > 0 ? wave : 1;
 }
 
@@ -647,7 +711,7 @@ Scratch scratch_of(void* p, int E, int n_seq, int blocks, size_t* bytes) {
   const size_t se = (size_t)n_seq * E;
   s.psum = reinterpret_cast<unsigned long long*>(take(se * 8));
   s.cnt = reinterpret_cast<int32_t*>(take(se * 4));
-  s.head = reinterpret_cast<uint32_t*>(take((size_t)n_seq * 16));
+  s.head = reinterpret_cast<unsigned long long*>(take((size_t)n_seq * 8));
   s.done = reinterpret_cast<uint32_t*>(take(4));
   s.zpart = reinterpret_cast<float*>(take((size_t)blocks * 4));
   s.bal_seq = reinterpret_cast<float*>(take((size_t)n_seq * 4));
@@ -685,7 +749,7 @@ struct BalanceArgs {
 template <int LPR, int NPL, bool FULL>
 cudaError_t run_balance(const BalanceArgs& a, cudaStream_t stream) {
   const int L = a.T / a.n_seq;
-  const int chunks = chunks_of(L, a.n_seq, a.E);
+  const int chunks = chunks_of(L, a.n_seq, LPR, blocks_per_sm(NPL));
   const Scratch s = scratch_of(a.scratch, a.E, a.n_seq, a.n_seq * chunks, nullptr);
   // L probabilities of at most 1 sum to at most 2^bits, so 2^61 in fixed point
   int bits = 0;
@@ -702,7 +766,7 @@ cudaError_t run_balance(const BalanceArgs& a, cudaStream_t stream) {
 template <int LPR, int NPL, bool FULL>
 cudaError_t run_route_backward(const RouteBackwardArgs& a, cudaStream_t stream) {
   const int L = a.T / a.n_seq;
-  const int chunks = chunks_of(L, a.n_seq, a.E);
+  const int chunks = chunks_of(L, a.n_seq, LPR, back_blocks_per_sm(LPR, NPL));
   const bool aux = a.grad_losses != nullptr;
   const size_t smem =
       4 * ((aux ? a.E : 0) +
@@ -719,7 +783,8 @@ cudaError_t run_route_backward(const RouteBackwardArgs& a, cudaStream_t stream) 
 
 size_t balance_loss_scratch_bytes(int T, int E, int n_seq) {
   const int L = T / n_seq;
-  const int chunks = L > 0 ? chunks_of(L, n_seq, E) : 1;
+  const Shape sh = shape_of(E);
+  const int chunks = L > 0 ? chunks_of(L, n_seq, sh.lpr, blocks_per_sm(sh.npl)) : 1;
   size_t bytes = 0;
   scratch_of(nullptr, E, n_seq, n_seq * chunks, &bytes);
   return bytes;
