@@ -74,32 +74,24 @@ MOE_DEVICE float rcp(float x) {
   return r;
 }
 
-// 1 - sigmoid(l)
-MOE_DEVICE float sigmoid_tail(float l) {
-  const float a = ex2(-fabsf(l) * kLog2E);
-  return (l > 0.f ? a : 1.f) * rcp(1.f + a);
-}
+// 1 / (1 + e^-l): e^-l past the largest float makes it 0
+MOE_DEVICE float sigmoid_fast(float l) { return rcp(1.f + ex2(-l * kLog2E)); }
 
-// The lane's sum of e^(v[i] - m), which STORE leaves in v.  Folding m into one
-// multiply-add rounds m log2(e) once, a factor that all columns share: it
-// cancels in a ratio and shifts the sum's logarithm by at most |m| 2^-24.
-// Maxima past 10^4 -- rows of the type's lowest value among them, where the
-// folded product overflows -- take the difference first.
+// The rows' code is straight-line: the kernels are short, and instructions
+// fetched for the first time cost more than those that a rare case would save.
+
+// The lane's sum of e^(v[i] - m), which STORE leaves in v.
 template <bool STORE, int NPL>
 MOE_DEVICE float exp_row(float (&v)[NPL], float m) {
   float2 s = pair(0.f);
-  const bool fold = fabsf(m) <= 1e4f;
-  const float2 ml = pair(-m * kLog2E);
 #pragma unroll
   for (int i = 0; i < NPL; i += 2) {
-    float2 x = make_float2(v[i], v[i + 1]);
-    if (fold) x = fma2(x, pair(kLog2E), ml);
-    else x = make_float2((x.x - m) * kLog2E, (x.y - m) * kLog2E);
-    x = make_float2(ex2(x.x), ex2(x.y));
-    s = add2(s, x);
+    const float2 x = mul2(add2(make_float2(v[i], v[i + 1]), pair(-m)), pair(kLog2E));
+    const float2 e = make_float2(ex2(x.x), ex2(x.y));
+    s = add2(s, e);
     if constexpr (STORE) {
-      v[i] = x.x;
-      v[i + 1] = x.y;
+      v[i] = e.x;
+      v[i + 1] = e.y;
     }
   }
   return s.x + s.y;
@@ -115,27 +107,23 @@ MOE_DEVICE float row_max(const float (&v)[NPL]) {
   return m == kNegInf ? 0.f : m;
 }
 
-// Mode 1: v[i] <- sigmoid(v[i]) e^c with c = max(0, -m), the common factor
-// cancels in a ratio and keeps rows of very negative logits from vanishing;
-// returns the sum over the lane's columns.
+// Mode 1: u[i] <- sigmoid(v[i]), or sigmoid(v[i] - m - 60) for a row whose
+// maximum m lies below -60: there sigmoid(l) is e^l to 26 digits, so the shift
+// is a common factor, which cancels in a ratio and keeps the row from
+// vanishing.  Returns the lane's sum.
 template <int NPL>
-MOE_DEVICE float sigmoid_row(float (&v)[NPL], float m) {
-  float s = 0.f;
-  if (m >= 0.f) {
+MOE_DEVICE float sigmoid_row(const float (&v)[NPL], float m, float (&u)[NPL]) {
+  const float2 d = pair(m < -60.f ? -(m + 60.f) : 0.f);
+  float2 s = pair(0.f);
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const float a = ex2(-fabsf(v[i]) * kLog2E);
-      v[i] = (v[i] > 0.f ? 1.f : a) * rcp(1.f + a);
-      s += v[i];
-    }
-  } else {  // every logit is negative
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      v[i] = ex2((v[i] - m) * kLog2E) * rcp(1.f + ex2(v[i] * kLog2E));
-      s += v[i];
-    }
+  for (int i = 0; i < NPL; i += 2) {
+    const float2 x = mul2(add2(make_float2(v[i], v[i + 1]), d), pair(-kLog2E));
+    const float2 t = add2(make_float2(ex2(x.x), ex2(x.y)), pair(1.f));
+    u[i] = rcp(t.x);
+    u[i + 1] = rcp(t.y);
+    s = add2(s, make_float2(u[i], u[i + 1]));
   }
-  return s;
+  return s.x + s.y;
 }
 
 // 1 / s, 0 for an empty row's sum
@@ -249,7 +237,13 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
     z = fmaf(lse, lse, z);
     keep_s = 0.f;
   };
-  auto row_step = [&](float(&v)[NPL], int(&id)[KPL], float(&nx)[NPL], int(&idn)[KPL]) {
+  float v[NPL];
+  int id[KPL];
+  load(r, on, v, id);
+#pragma unroll 1
+  for (int rb = rw; rb < L; rb += stride) {
+    float nx[NPL];
+    int idn[KPL];
     load(r + stride, on1, nx, idn);
     const bool on2 = kept_row(r + 2 * stride);
     if (__any_sync(0xffffffffu, on)) {  // else the warp's rows are padding
@@ -260,7 +254,7 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
         inv = inverse(s);
       } else {
         s = group_sum<LPR>(exp_row<false>(v, m));
-        inv = inverse(group_sum<LPR>(sigmoid_row(v, m)));
+        inv = inverse(group_sum<LPR>(sigmoid_row(v, m, v)));
       }
       // a row left out is all -inf and adds zeros
 #pragma unroll
@@ -285,18 +279,13 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
       }
     }
     if (++it % LPR == 0) add_z();
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = nx[i];
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) id[j] = idn[j];
     on = on1;
     on1 = on2;
     r += stride;
-  };
-  float va[NPL], vb[NPL];
-  int ia[KPL], ib[KPL];
-  load(r, on, va, ia);
-  for (int rb = rw; rb < L;) {
-    row_step(va, ia, vb, ib);
-    if ((rb += stride) >= L) break;
-    row_step(vb, ib, va, ia);
-    rb += stride;
   }
   add_z();
   // the warp's rows, then the block's warps in order
@@ -489,8 +478,8 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
   const int rw = chunk * kStep + warp * RPW;
   int r = rw + sub;
   bool on = kept_row(r), on1 = kept_row(r + stride);
-  float va[NPL], vb[NPL];
-  if constexpr (AUX) load_row<LPR, NPL, FULL>(a.logits + (t0 + r) * a.ld, E, lig, on, va);
+  float v[NPL];
+  if constexpr (AUX) load_row<LPR, NPL, FULL>(a.logits + (t0 + r) * a.ld, E, lig, on, v);
 
   float gz = 0.f;
   if constexpr (AUX) {
@@ -506,43 +495,38 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
   const float inv_scale = !kSigmoid ? 1.f : a.scale != 0.f ? 1.f / a.scale : 0.f;
   __syncthreads();
 
-  auto row_step = [&](float(&v)[NPL], float(&nx)[NPL]) {
+#pragma unroll 1
+  for (int rb = rw; rb < L; rb += stride) {
+    float nx[NPL];
     if constexpr (AUX)
       load_row<LPR, NPL, FULL>(a.logits + (t0 + r + stride) * a.ld, E, lig, on1, nx);
     const bool on2 = kept_row(r + 2 * stride);
     const size_t t = t0 + r;
-    const bool in = r < L, now = on;
+    const bool in = r < L;
     float* out = a.dlogits + t * a.ld_d;
-    on = on1;
-    on1 = on2;
-    r += stride;
-    if (!__any_sync(0xffffffffu, now)) {  // the warp's rows are padding
+    if (!__any_sync(0xffffffffu, on)) {  // the warp's rows are padding
       if (in) {
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
           if (FULL || lig + LPR * i < E) out[lig + LPR * i] = 0.f;
         if (a.d_shared_gate && lig == 0) out[E] = 0.f;
       }
-      return;
-    }
+    } else {
     int id[KPL];
     float wk[KPL], gk[KPL];
     if (routing) {
 #pragma unroll
       for (int j = 0; j < KPL; ++j) {
         const int k = lig + LPR * j;
-        const bool have = now && k < K;
+        const bool have = on && k < K;
         id[j] = have ? __ldg(a.ids + t * K + k) : -1;
         wk[j] = have ? __ldg(a.weights + t * K + k) : 0.f;
         gk[j] = have ? __ldg(a.d_weights + t * K + k) : 0.f;
       }
     }
-    // mode 0: e^(v - max); mode 1: the smaller of sigmoid and 1 - sigmoid,
-    // from which both follow without cancellation, or for a row of negative
-    // logits alone the scaled sigmoid
+    // mode 0: e^(v - max); mode 1: the (scaled) sigmoids
     float x[NPL];
     float m = 0.f, lse = 0.f, inv = 0.f, inv_exp = 0.f, dot = 0.f;
-    bool pos = true;
     if constexpr (AUX) {
       m = row_max<LPR, NPL>(v);
       if constexpr (!kSigmoid) {
@@ -555,32 +539,13 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
         inv_exp = inverse(s);
       }
       if constexpr (kSigmoid) {
-        pos = m >= 0.f;
-        float s = 0.f;
-        if (pos) {
-#pragma unroll
-          for (int i = 0; i < NPL; ++i) {
-            const float e = ex2(-fabsf(v[i]) * kLog2E);
-            x[i] = e * rcp(1.f + e);
-            const float sg = v[i] > 0.f ? 1.f - x[i] : x[i];
-            s += sg;
-            if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], sg, dot);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < NPL; ++i) x[i] = v[i];
-          s = sigmoid_row(x, m);
-#pragma unroll
-          for (int i = 0; i < NPL; ++i)
-            if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], x[i], dot);
-        }
-        inv = inverse(group_sum<LPR>(s));
+        inv = inverse(group_sum<LPR>(sigmoid_row(v, m, x)));
       } else {
         inv = inv_exp;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-          if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], x[i], dot);
       }
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], x[i], dot);
       dot = group_sum<LPR>(dot) * inv;
     }
     if (routing) {
@@ -589,7 +554,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       int* tag = reinterpret_cast<int*>(buf);
 #pragma unroll
       for (int j = 0; j < KPL; ++j) {
-        if (now && lig + LPR * j < K && (unsigned)id[j] >= (unsigned)E) {
+        if (on && lig + LPR * j < K && (unsigned)id[j] >= (unsigned)E) {
           moe_set_status(a.dev_status, MOE_DEV_BAD_EXPERT_ID);
           id[j] = -1;
         }
@@ -603,7 +568,8 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
         gk[j] = wk[j] * (gk[j] - wg);
         if (id[j] < 0) continue;
         lost |= tag[id[j]] != lig + LPR * j + 1;
-        if constexpr (kSigmoid && !AUX) gk[j] *= sigmoid_tail(__ldg(a.logits + t * a.ld + id[j]));
+        if constexpr (kSigmoid && !AUX)
+          gk[j] *= 1.f - sigmoid_fast(__ldg(a.logits + t * a.ld + id[j]));
       }
       // top-K gives distinct ids: every replica found its own tag and the
       // values go out together; a repeated id adds up in k order instead
@@ -637,14 +603,11 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       if constexpr (AUX && !kSigmoid) {
         d = fmaf(x[i], fmaf(smem[c], inv, shift), d);
       } else if constexpr (AUX) {
-        const float other = 1.f - x[i];
-        const bool up = v[i] > 0.f;
-        const float sg = pos && up ? other : x[i];
-        const float tail = !pos ? rcp(1.f + ex2(v[i] * kLog2E)) : up ? x[i] : other;
-        d = fmaf(sg, fmaf(smem[c], inv, shift), d) * tail;
+        // 1 - x is 1 - sigmoid for shifted rows too: 1
+        d = fmaf(x[i], fmaf(smem[c], inv, shift), d) * (1.f - x[i]);
         if (gz != 0.f) d = fmaf(zq, ex2((v[i] - m) * kLog2E), d);
       }
-      if (in) out[c] = now ? d : 0.f;
+      if (RPW == 1 || in) out[c] = RPW == 1 || on ? d : 0.f;
     }
     if (routing) {
       __syncwarp();
@@ -655,7 +618,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
     }
     if (a.d_shared_gate && in && lig == 0) {
       float g = 0.f;
-      if (now) {
+      if (on) {
         const float l = __ldg(a.logits + t * a.ld + E);
         const float ea = expf(-fabsf(l));
         const float q = 1.f / (1.f + ea);
@@ -663,12 +626,14 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       }
       out[E] = g;
     }
-  };
-  for (int rb = rw; rb < L;) {
-    row_step(va, vb);
-    if ((rb += stride) >= L) break;
-    row_step(vb, va);
-    rb += stride;
+    }
+    if constexpr (AUX) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) v[i] = nx[i];
+    }
+    on = on1;
+    on1 = on2;
+    r += stride;
   }
 }
 
