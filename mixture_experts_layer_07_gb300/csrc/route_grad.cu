@@ -40,7 +40,7 @@ struct Scratch {
   unsigned long long* psum;  // [n_seq][E] fixed-point sums
   int32_t* cnt;              // [n_seq][E]
   unsigned long long* head;  // [n_seq]: blocks done << 48 | blocks with a NaN << 32 | kept tokens
-  uint32_t* done;            // sequences done
+  unsigned long long* done;  // sequences done
   float* zpart;              // [blocks] sums of lse^2
   float* bal_seq;            // [n_seq]
   float* z_seq;              // [n_seq]
@@ -143,6 +143,12 @@ MOE_DEVICE void load_row(const float* __restrict__ row, int E, int lig, bool on,
   }
 }
 
+MOE_DEVICE unsigned long long add_acq_rel(unsigned long long* p, unsigned long long v) {
+  unsigned long long old;
+  asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(old) : "l"(p), "l"(v) : "memory");
+  return old;
+}
+
 // Sums of a pair over the block; `red` is free again after the next barrier.
 template <typename A, typename B>
 struct Pair {
@@ -190,7 +196,7 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
                float* __restrict__ mean_prob, int32_t* __restrict__ valid,
                float* __restrict__ losses, int32_t* __restrict__ dev_status) {
   constexpr int RPW = 32 / LPR;
-  constexpr int KPL = 32 / LPR;  // replicas of a token per lane, K <= 32
+  constexpr int KPL = NPL < 32 / LPR ? NPL : 32 / LPR;  // replicas per lane, K <= min(E, 32)
   constexpr int kStep = kWarps * RPW;
   extern __shared__ float smem[];
   float* psm = smem;                                              // [kWarps][E]
@@ -319,12 +325,10 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
     }
     if (tid == 0) sc.zpart[blockIdx.x] = z;
     __syncthreads();
-    if (tid == 0) {  // fences of one thread order the whole block's work, by the barriers
+    if (tid == 0) {  // one thread's release and acquire order the block's work, by the barriers
       const unsigned long long mine =
           1ull << 48 | (unsigned long long)poisoned << 32 | (unsigned)nv;
-      __threadfence();
-      total_s = atomicAdd(head, mine) + mine;
-      __threadfence();
+      total_s = add_acq_rel(head, mine) + mine;
     }
     __syncthreads();
     if (total_s >> 48 != (unsigned)chunks) return;
@@ -397,9 +401,7 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
     sc.z_seq[seq] = z;
     valid[seq] = nv;
     if (chunks > 1) *head = 0;
-    __threadfence();
-    last = atomicAdd(sc.done, 1u) == (uint32_t)(n_seq - 1);
-    __threadfence();
+    last = add_acq_rel(sc.done, 1ull) == (unsigned long long)(n_seq - 1);
   }
   __syncthreads();
   if (!last) return;
@@ -455,7 +457,7 @@ template <int LPR, int NPL, int MODE, bool AUX, bool FULL>
 __global__ void __launch_bounds__(kThreads, back_blocks_per_sm(LPR, NPL))
 route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
   constexpr int RPW = 32 / LPR;
-  constexpr int KPL = 32 / LPR;  // replicas of a token per lane, K <= 32
+  constexpr int KPL = NPL < 32 / LPR ? NPL : 32 / LPR;  // replicas per lane, K <= min(E, 32)
   constexpr int kStep = kWarps * RPW;
   constexpr bool kSigmoid = MODE != MOE_SCORE_SOFTMAX_RENORM;
   extern __shared__ float smem[];
@@ -645,6 +647,7 @@ struct Shape {
   int lpr, npl;
 };
 Shape shape_of(int E) {
+  if (E <= 16) return {4, 4};
   if (E <= 32) return {8, 4};
   if (E <= 64) return {8, 8};
   if (E <= 128) return {8, 16};
@@ -677,7 +680,7 @@ Scratch scratch_of(void* p, int E, int n_seq, int blocks, size_t* bytes) {
   s.psum = reinterpret_cast<unsigned long long*>(take(se * 8));
   s.cnt = reinterpret_cast<int32_t*>(take(se * 4));
   s.head = reinterpret_cast<unsigned long long*>(take((size_t)n_seq * 8));
-  s.done = reinterpret_cast<uint32_t*>(take(4));
+  s.done = reinterpret_cast<unsigned long long*>(take(8));
   s.zpart = reinterpret_cast<float*>(take((size_t)blocks * 4));
   s.bal_seq = reinterpret_cast<float*>(take((size_t)n_seq * 4));
   s.z_seq = reinterpret_cast<float*>(take((size_t)n_seq * 4));
@@ -688,6 +691,7 @@ Scratch scratch_of(void* p, int E, int n_seq, int blocks, size_t* bytes) {
 // Calls f<LPR, NPL, FULL> for the shape of E.
 #define MOE_BY_SHAPE(f, E, ...)                                                                  \
   switch (shape_of(E).lpr * 64 + shape_of(E).npl) {                                              \
+    case 4 * 64 + 4: return (E) == 16 ? f<4, 4, true>(__VA_ARGS__) : f<4, 4, false>(__VA_ARGS__);     \
     case 8 * 64 + 4: return (E) == 32 ? f<8, 4, true>(__VA_ARGS__) : f<8, 4, false>(__VA_ARGS__);     \
     case 8 * 64 + 8: return (E) == 64 ? f<8, 8, true>(__VA_ARGS__) : f<8, 8, false>(__VA_ARGS__);     \
     case 8 * 64 + 16: return (E) == 128 ? f<8, 16, true>(__VA_ARGS__) : f<8, 16, false>(__VA_ARGS__); \

@@ -276,10 +276,13 @@ _E4M3 = (torch.float8_e4m3fn, torch.uint8)  # codes, as either
 
 
 def _pc(t, dtype, numel, name):
-    """Device pointer of a tensor (or None) that must hold `numel` values of `dtype`."""
+    """Device pointer of a tensor (or None) that must hold `numel` values of `dtype` (or of one
+    of several)."""
     if t is None:
         return None
-    if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
+    if t.dtype is dtype and t.numel() == numel and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
     if t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous tensor of {numel} values expected, got shape "
