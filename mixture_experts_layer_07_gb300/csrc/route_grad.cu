@@ -210,6 +210,7 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
   const int stride = chunks * kStep;
   const size_t t0 = (size_t)seq * L;
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
+  auto some = [&](int j) { return j == 0 || LPR * j < K; };  // the warp has a replica LPR*j + ...
   const int lig = lane % LPR, sub = lane / LPR;
   for (int e = tid; e < E; e += kThreads) hist[e] = 0;
   if (tid == 0) bad = 0;
@@ -225,7 +226,7 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
     load_row<LPR, NPL, FULL>(logits + (t0 + r) * ld, E, lig, on, v);
 #pragma unroll
     for (int j = 0; j < KPL; ++j)
-      id[j] = on && lig + LPR * j < K ? __ldg(ids + (t0 + r) * K + lig + LPR * j) : 0;
+      if (some(j)) id[j] = on && lig + LPR * j < K ? __ldg(ids + (t0 + r) * K + lig + LPR * j) : 0;
   };
   const int rw = chunk * kStep + warp * RPW;
   int r = rw + sub;
@@ -278,7 +279,7 @@ balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restri
         nan |= !(inv == inv);
 #pragma unroll
         for (int j = 0; j < KPL; ++j)
-          if (lig + LPR * j < K) {
+          if (some(j) && lig + LPR * j < K) {
             if ((unsigned)id[j] < (unsigned)E) atomicAdd(&hist[id[j]], 1);
             else moe_set_status(dev_status, MOE_DEV_BAD_EXPERT_ID);
           }
@@ -465,6 +466,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
   const int warp = warp_id(), lane = lane_id();
   const int lig = lane % LPR, sub = lane / LPR;
   const bool routing = a.d_weights != nullptr;
+  auto some = [&](int j) { return j == 0 || LPR * j < K; };
   // a_e of this sequence (AUX), then the row's routing gradient, zero between rows
   float* buf = smem + (AUX ? E : 0) + (size_t)(warp * RPW + sub) * buf_stride(E, LPR);
   const int seq = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
@@ -519,6 +521,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
     if (routing) {
 #pragma unroll
       for (int j = 0; j < KPL; ++j) {
+        if (!some(j)) continue;
         const int k = lig + LPR * j;
         const bool have = on && k < K;
         id[j] = have ? __ldg(a.ids + t * K + k) : -1;
@@ -556,6 +559,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       int* tag = reinterpret_cast<int*>(buf);
 #pragma unroll
       for (int j = 0; j < KPL; ++j) {
+        if (!some(j)) continue;
         if (on && lig + LPR * j < K && (unsigned)id[j] >= (unsigned)E) {
           moe_set_status(a.dev_status, MOE_DEV_BAD_EXPERT_ID);
           id[j] = -1;
@@ -567,6 +571,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < KPL; ++j) {
+        if (!some(j)) continue;
         gk[j] = wk[j] * (gk[j] - wg);
         if (id[j] < 0) continue;
         lost |= tag[id[j]] != lig + LPR * j + 1;
@@ -578,11 +583,11 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       if (!__any_sync(0xffffffffu, lost)) {
 #pragma unroll
         for (int j = 0; j < KPL; ++j)
-          if (id[j] >= 0) buf[id[j]] = gk[j];
+          if (some(j) && id[j] >= 0) buf[id[j]] = gk[j];
       } else {
 #pragma unroll
         for (int j = 0; j < KPL; ++j)
-          if (id[j] >= 0) buf[id[j]] = 0.f;
+          if (some(j) && id[j] >= 0) buf[id[j]] = 0.f;
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < KPL; ++j)
@@ -615,7 +620,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < KPL; ++j)
-        if (id[j] >= 0) buf[id[j]] = 0.f;
+        if (some(j) && id[j] >= 0) buf[id[j]] = 0.f;
       __syncwarp();
     }
     if (a.d_shared_gate && in && lig == 0) {
