@@ -527,6 +527,23 @@ moe_status_t moe_layer(const moe_config_t* cfg, int T, const void* x, const moe_
                        int32_t* dev_status, moe_stream_t stream);
 
 /*
+ * moe_layer for W8A8 experts (wdtype MOE_W8A8_FP8E4M3_B128, else
+ * MOE_ERR_UNSUPPORTED) whose 8-bit activations exist already, as
+ * moe_add_rmsnorm writes them: the router and the shared expert read x, the
+ * experts read the codes, which are permuted as they are (1 byte per value, no
+ * bf16 copy of the permuted rows and no quantising pass before G1).  With the
+ * codes and scales that the W8A8 quantiser gives for x, the result is that of
+ * moe_layer bit for bit.  The workspace's xp is not written.
+ *   xq        [T, H] e4m3, 16-byte aligned
+ *   xq_scale  [T, ceil(H / 128)] fp32
+ * Everything else as moe_layer.
+ */
+moe_status_t moe_layer_q8(const moe_config_t* cfg, int T, const void* x, const void* xq,
+                          const float* xq_scale, const moe_weights_t* w, void* out,
+                          void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                          moe_stream_t stream);
+
+/*
  * Byte offsets of the intermediates inside a moe_layer workspace, for callers
  * that inspect them (tests, profilers).  Filled for cfg and T_max.
  */

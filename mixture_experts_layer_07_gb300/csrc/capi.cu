@@ -153,6 +153,10 @@ void layout_of(const moe_config_t* c, moe_workspace_layout_t* L) {
   L->total = off;
 }
 
+moe_status_t run_layer(const moe_config_t* cfg, int T, const void* x, const void* xq,
+                       const float* xq_scale, const moe_weights_t* w, void* out, void* workspace,
+                       size_t workspace_bytes, int32_t* dev_status, moe_stream_t stream);
+
 }  // namespace
 
 extern "C" {
@@ -447,6 +451,34 @@ moe_status_t moe_workspace_bytes(const moe_config_t* cfg, size_t* bytes) {
 moe_status_t moe_layer(const moe_config_t* cfg, int T, const void* x, const moe_weights_t* w,
                        void* out, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                        moe_stream_t stream) {
+  return run_layer(cfg, T, x, nullptr, nullptr, w, out, workspace, workspace_bytes, dev_status,
+                   stream);
+}
+
+moe_status_t moe_layer_q8(const moe_config_t* cfg, int T, const void* x, const void* xq,
+                          const float* xq_scale, const moe_weights_t* w, void* out,
+                          void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                          moe_stream_t stream) {
+  const moe_status_t s = check_cfg(cfg);
+  if (s != MOE_OK) return s;
+  if (cfg->wdtype != MOE_W8A8_FP8E4M3_B128) return MOE_ERR_UNSUPPORTED;
+  if (T < 0 || T > cfg->T_max) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!xq || !xq_scale) return MOE_ERR_INVALID_ARG;
+  if (misaligned(xq, 16) || misaligned(xq_scale, 4)) return MOE_ERR_MISALIGNED;
+  return run_layer(cfg, T, x, xq, xq_scale, w, out, workspace, workspace_bytes, dev_status,
+                   stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// moe_layer, and with xq / xq_scale moe_layer_q8: the experts read these codes
+// instead of quantising the permuted x.
+moe_status_t run_layer(const moe_config_t* cfg, int T, const void* x, const void* xq,
+                       const float* xq_scale, const moe_weights_t* w, void* out, void* workspace,
+                       size_t workspace_bytes, int32_t* dev_status, moe_stream_t stream) {
   moe_status_t s = check_cfg(cfg);
   if (s != MOE_OK) return s;
   if (T < 0 || T > cfg->T_max) return MOE_ERR_INVALID_ARG;
@@ -587,7 +619,13 @@ moe_status_t moe_layer(const moe_config_t* cfg, int T, const void* x, const moe_
   // it -- gpt-oss-20b shape T=32: 217 -> 308 us)
   const bool gather = decode && cfg->dispatch != MOE_DISPATCH_SIMT &&
                       cfg->wdtype == MOE_W_BF16;
-  if (!gather) {
+  if (xq) {
+    const W8a8Rows rows =
+        w8a8_rows(ws + L.gemm_scratch + grouped_gemm_scratch_bytes(R, E), R, H);
+    e = launch_permute_copy_q8(xq, xq_scale, f2r, T, K, H, rows.codes, rows.scales, stream);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    xp = nullptr;
+  } else if (!gather) {
     e = launch_permute_copy(x, f2r, T, K, H, xp, stream);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
   }
@@ -611,7 +649,9 @@ moe_status_t moe_layer(const moe_config_t* cfg, int T, const void* x, const moe_
   return cuda_status(e);
 }
 
-}  // extern "C"
+}  // namespace
+
+extern "C" {
 
 moe_status_t moe_bounded_wait_check(const int32_t* counter, int target, int limit_us,
                                     int32_t* dev_status, moe_stream_t stream) {
@@ -619,3 +659,5 @@ moe_status_t moe_bounded_wait_check(const int32_t* counter, int target, int limi
   return cuda_status(launch_bounded_wait_check(counter, target, (uint64_t)limit_us * 1000,
                                                dev_status, static_cast<cudaStream_t>(stream)));
 }
+
+}  // extern "C"

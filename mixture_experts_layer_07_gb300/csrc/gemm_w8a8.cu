@@ -509,17 +509,22 @@ size_t w8a8_act_bytes(int R, int H, int I) {
          moe_align_up(r * I, 256) + moe_align_up(r * moe_cdiv(I, 128) * 4, 256);
 }
 
+W8a8Rows w8a8_rows(void* act_scratch, int R, int H) {
+  char* p = static_cast<char*>(act_scratch);
+  return {reinterpret_cast<uint8_t*>(p),
+          reinterpret_cast<float*>(p + moe_align_up((size_t)R * H, 256))};
+}
+
 cudaError_t launch_w8a8(const void* xp, int R, int E_blocks, int H, int I, const void* w1,
                         const void* w3, const void* w2, const float* s1, const float* s3,
                         const float* s2, void* hact, void* y, const int32_t* counts,
                         const int4* tile_items, void* act_scratch, int32_t* dev_status,
                         cudaStream_t stream) {
   if (R <= 0) return cudaSuccess;
-  char* p = static_cast<char*>(act_scratch);
-  uint8_t* xq = reinterpret_cast<uint8_t*>(p);
-  p += moe_align_up((size_t)R * H, 256);
-  float* sx = reinterpret_cast<float*>(p);
-  p += moe_align_up((size_t)R * moe_cdiv(H, 128) * 4, 256);
+  const W8a8Rows rows = w8a8_rows(act_scratch, R, H);
+  uint8_t* xq = rows.codes;
+  float* sx = rows.scales;
+  char* p = reinterpret_cast<char*>(sx) + moe_align_up((size_t)R * moe_cdiv(H, 128) * 4, 256);
   uint8_t* hq = reinterpret_cast<uint8_t*>(p);
   p += moe_align_up((size_t)R * I, 256);
   float* sh = reinterpret_cast<float*>(p);
@@ -529,7 +534,7 @@ cudaError_t launch_w8a8(const void* xp, int R, int E_blocks, int H, int I, const
       !w8_weight_map(&m_w2, w2, E_blocks, H, I) || !w8_act_map(&m_x, xq, R, H, W8Cfg<true>::BN) ||
       !w8_act_map(&m_h, hq, R, I, W8Cfg<false>::BN))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_quant(xp, R, H, xq, sx, stream);
+  cudaError_t e = xp ? launch_quant(xp, R, H, xq, sx, stream) : cudaSuccess;
   if (e != cudaSuccess) return e;
   e = launch_gemm<true>(m_w1, m_w3, m_x, s1, s3, sx, counts, tile_items, I, H, R, hact,
                         dev_status, stream);

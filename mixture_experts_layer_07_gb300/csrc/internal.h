@@ -34,6 +34,13 @@ size_t grouped_gemm_scratch_bytes_ex(int R, int E_blocks, int H, int I, int wdty
 // per-(row, 128 columns) scales live in act_scratch (w8a8_act_bytes of it);
 // the plan's tile list (every non-empty block, 128-row items) drives both GEMMs
 size_t w8a8_act_bytes(int R, int H, int I);
+struct W8a8Rows {
+  uint8_t* codes;  // [R][H]
+  float* scales;   // [R][ceil(H / 128)]
+};
+// where in act_scratch the e4m3 copy of xp lies; with xp NULL launch_w8a8 takes
+// it as the caller left it there
+W8a8Rows w8a8_rows(void* act_scratch, int R, int H);
 cudaError_t launch_w8a8(const void* xp, int R, int E_blocks, int H, int I, const void* w1,
                         const void* w3, const void* w2, const float* s1, const float* s3,
                         const float* s2, void* hact, void* y, const int32_t* counts,
@@ -65,6 +72,10 @@ cudaError_t launch_bounded_wait_check(const int32_t* counter, int target, uint64
                                       int32_t* dev_status, cudaStream_t stream);
 cudaError_t launch_permute_copy(const void* x, const int32_t* flat_to_row, int T, int K, int H,
                                 void* xp, cudaStream_t stream);
+// the same for e4m3 rows with their scales per 128 columns
+cudaError_t launch_permute_copy_q8(const void* xq, const float* xs, const int32_t* flat_to_row,
+                                   int T, int K, int H, void* xqp, float* xsp,
+                                   cudaStream_t stream);
 
 // Fused decode routing (T <= kRouteDecodeMaxT): router + top-K + permute +
 // grouped-GEMM plan in one launch.  done_ctr must be zero before the launch

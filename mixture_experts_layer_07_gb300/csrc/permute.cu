@@ -221,6 +221,47 @@ permute_copy_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ fla
   }
 }
 
+// The same for rows quantised before the permute: H16 16-byte vectors of codes
+// and KB scales per row.
+__global__ void __launch_bounds__(256)
+permute_copy_q8_kernel(const uint4* __restrict__ xq, const float* __restrict__ xs,
+                       const int32_t* __restrict__ flat_to_row, int T, int K, int H16, int KB,
+                       uint4* __restrict__ xqp, float* __restrict__ xsp) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = lane_id();
+  for (int t = blockIdx.x * 8 + warp_id(); t < T; t += gridDim.x * 8) {
+    const int myrow = lane < K ? __ldg(flat_to_row + (size_t)t * K + lane) : -1;
+    const uint4* src = xq + (size_t)t * H16;
+    const float* ssrc = xs + (size_t)t * KB;
+    for (int c0 = 0; c0 < H16; c0 += 32 * 8) {
+      uint4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = c0 + j * 32 + lane;
+        if (c < H16) v[j] = __ldg(src + c);
+      }
+      for (int k = 0; k < K; ++k) {
+        const int r = __shfl_sync(0xffffffffu, myrow, k);
+        if (r < 0) continue;
+        uint4* dst = xqp + (size_t)r * H16;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = c0 + j * 32 + lane;
+          if (c < H16) dst[c] = v[j];
+        }
+      }
+    }
+    for (int b0 = 0; b0 < KB; b0 += 32) {
+      const float s = b0 + lane < KB ? __ldg(ssrc + b0 + lane) : 0.f;
+      for (int k = 0; k < K; ++k) {
+        const int r = __shfl_sync(0xffffffffu, myrow, k);
+        if (r >= 0 && b0 + lane < KB) xsp[(size_t)r * KB + b0 + lane] = s;
+      }
+    }
+  }
+}
+
 }  // namespace
 
 namespace {
@@ -238,6 +279,15 @@ cudaError_t launch_copy(const void* x, const int32_t* flat_to_row, int T, int K,
 cudaError_t launch_permute_copy(const void* x, const int32_t* flat_to_row, int T, int K, int H,
                                 void* xp, cudaStream_t stream) {
   return launch_copy(x, flat_to_row, T, K, H, xp, stream);
+}
+
+cudaError_t launch_permute_copy_q8(const void* xq, const float* xs, const int32_t* flat_to_row,
+                                   int T, int K, int H, void* xqp, float* xsp,
+                                   cudaStream_t stream) {
+  const int grid = moe_cdiv(T, 8) < 152 * 16 ? moe_cdiv(T, 8) : 152 * 16;
+  return moe_launch(permute_copy_q8_kernel, dim3(grid), dim3(256), 0, stream, 1,
+                    static_cast<const uint4*>(xq), xs, flat_to_row, T, K, H / 16,
+                    moe_cdiv(H, 128), static_cast<uint4*>(xqp), xsp);
 }
 
 size_t permute_scratch_bytes(int T, int E, int K) {

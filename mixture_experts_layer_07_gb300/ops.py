@@ -36,7 +36,7 @@ EXPORTS = ["moe_status_string", "moe_default_m_skinny", "moe_block_variant", "mo
            "moe_router_tc_scratch_bytes", "moe_router_gemm_tc", "moe_bounded_wait_check",
            "moe_add_rmsnorm", "moe_add_rmsnorm_backward_scratch_bytes",
            "moe_add_rmsnorm_backward", "moe_balance_loss_scratch_bytes", "moe_balance_loss",
-           "moe_route_backward", "moe_unpermute_backward"]
+           "moe_route_backward", "moe_unpermute_backward", "moe_layer_q8"]
 
 PERMUTE_STATIC_SCRATCH_BYTES = 1 << 20
 DT_BF16, DT_F32 = 0, 1
@@ -106,6 +106,8 @@ def _lib():
             "moe_layer": [ctypes.POINTER(Config), _I, _P, ctypes.POINTER(Weights), _P, _P, _S,
                           _P, _P],
             "moe_bounded_wait_check": [_P, _I, _I, _P, _P],
+            "moe_layer_q8": [ctypes.POINTER(Config), _I, _P, _P, _P, ctypes.POINTER(Weights), _P,
+                             _P, _S, _P, _P],
             "moe_add_rmsnorm": [_P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _P, _P, _I, _P],
             "moe_add_rmsnorm_backward_scratch_bytes": [_I, _I, ctypes.POINTER(_S)],
             "moe_add_rmsnorm_backward": [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _S, _P],
@@ -387,6 +389,18 @@ def layer(cfg: Config, x, weights: Weights, out, workspace, dev_status=None, str
            "moe_layer")
 
 
+def layer_q8(cfg: Config, x, xq, xq_scale, weights: Weights, out, workspace, dev_status=None,
+             stream=None):
+    """moe_layer on activations that are e4m3 codes already (W8A8 experts; see the header)."""
+    T, H = x.shape
+    _check(_lib().moe_layer_q8(ctypes.byref(cfg), T, _pc(x, _BF16, T * cfg.H, "x"),
+                               _pc(xq, _E4M3, T * cfg.H, "xq"),
+                               _pc(xq_scale, _F32, T * -(-cfg.H // 128), "xq_scale"),
+                               ctypes.byref(weights), _pc(out, _BF16, T * cfg.H, "out"),
+                               _p(workspace), workspace.numel(), _p(dev_status),
+                               _stream(stream)), "moe_layer_q8")
+
+
 class MoELayer:
     """Owns the config, the device workspace and the weight pointers of one
     layer and calls ``moe_layer``.  Tensors are kept referenced so their
@@ -418,6 +432,38 @@ class MoELayer:
             n *= s
         nbytes = n * torch.empty((), dtype=dtype).element_size()
         return self.workspace[off:off + nbytes].view(dtype).view(*shape)
+
+
+class MoEBlock:
+    """A pre-norm block: h = x + residual, y = rmsnorm(h) * weight, out = MoELayer(y).
+
+    With W8A8 experts the norm also writes y's e4m3 codes and the layer reads those.  Calls with
+    up to cfg.T_max tokens; returns (out, h), of which h is the residual stream's next value."""
+
+    def __init__(self, cfg: Config, tensors: dict, norm_weight, eps=1e-6, device="cuda"):
+        self.layer = MoELayer(cfg, tensors, device)
+        self.norm_weight, self.eps = norm_weight, eps
+        T, H = cfg.T_max, cfg.H
+        self.y = torch.empty(T, H, dtype=torch.bfloat16, device=device)
+        self.q8 = cfg.wdtype == W8A8_FP8
+        if self.q8:
+            self.yq = torch.empty(T, H, dtype=torch.float8_e4m3fn, device=device)
+            self.yq_scale = torch.empty(T, -(-H // 128), dtype=torch.float32, device=device)
+
+    def __call__(self, x, residual=None, out=None, stream=None):
+        T = x.shape[0]
+        h = torch.empty_like(x) if residual is not None else None
+        out = torch.empty_like(x) if out is None else out
+        y, L = self.y[:T], self.layer
+        if self.q8:
+            yq, ys = self.yq[:T], self.yq_scale[:T]
+            add_rmsnorm(x, self.norm_weight, self.eps, y, residual=residual, h=h, yq=yq,
+                        yq_scale=ys, stream=stream)
+            layer_q8(L.cfg, y, yq, ys, L.weights, out, L.workspace, L.dev_status, stream)
+        else:
+            add_rmsnorm(x, self.norm_weight, self.eps, y, residual=residual, h=h, stream=stream)
+            layer(L.cfg, y, L.weights, out, L.workspace, L.dev_status, stream)
+        return out, (x if h is None else h)
 
 
 def bounded_wait_check(counter, target, limit_us, dev_status, stream=None):
