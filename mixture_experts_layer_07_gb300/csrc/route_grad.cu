@@ -107,13 +107,16 @@ MOE_DEVICE float row_max(const float (&v)[NPL]) {
   return m == kNegInf ? 0.f : m;
 }
 
-// Mode 1: u[i] <- sigmoid(v[i]), or sigmoid(v[i] - m - 60) for a row whose
-// maximum m lies below -60: there sigmoid(l) is e^l to 26 digits, so the shift
-// is a common factor, which cancels in a ratio and keeps the row from
-// vanishing.  Returns the lane's sum.
+// What mode 1 adds to the logits of a row with maximum m: nothing, or where m
+// lies below -60 what brings it there.  sigmoid(l) is e^l to 26 digits then, so
+// the shift is a common factor of the row's sigmoids, which cancels in a ratio
+// and keeps them from vanishing.
+MOE_DEVICE float row_shift(float m) { return m < -60.f ? -(m + 60.f) : 0.f; }
+
+// Mode 1: u[i] <- sigmoid(v[i] + row_shift).  Returns the lane's sum.
 template <int NPL>
 MOE_DEVICE float sigmoid_row(const float (&v)[NPL], float m, float (&u)[NPL]) {
-  const float2 d = pair(m < -60.f ? -(m + 60.f) : 0.f);
+  const float2 d = pair(row_shift(m));
   float2 s = pair(0.f);
 #pragma unroll
   for (int i = 0; i < NPL; i += 2) {
@@ -178,7 +181,7 @@ MOE_DEVICE void block_sums(Pair<A, B>* red, A& a, B& b) {
 // third row, and with few lanes per row several replicas per lane.
 constexpr int blocks_per_sm(int npl) { return npl <= 8 ? 4 : npl <= 16 ? 3 : 2; }
 constexpr int back_blocks_per_sm(int lpr, int npl) {
-  return npl <= 4 ? 4 : npl <= 16 ? 3 : 2;
+  return npl <= 4 ? 4 : npl <= 8 && lpr == 32 ? 4 : npl <= 16 ? 3 : 2;
 }
 
 // ---------------------------------------------------------------- forward
@@ -461,6 +464,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
   constexpr int KPL = NPL < 32 / LPR ? NPL : 32 / LPR;  // replicas per lane, K <= min(E, 32)
   constexpr int kStep = kWarps * RPW;
   constexpr bool kSigmoid = MODE != MOE_SCORE_SOFTMAX_RENORM;
+  constexpr bool kEarly = kSigmoid && AUX && KPL == 1;  // the selected logit loaded ahead of its use
   extern __shared__ float smem[];
   const int E = a.E, K = a.K;
   const int warp = warp_id(), lane = lane_id();
@@ -517,7 +521,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       }
     } else {
     int id[KPL];
-    float wk[KPL], gk[KPL];
+    float wk[KPL], gk[KPL], lk = 0.f;
     if (routing) {
 #pragma unroll
       for (int j = 0; j < KPL; ++j) {
@@ -529,7 +533,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
         gk[j] = have ? __ldg(a.d_weights + t * K + k) : 0.f;
       }
     }
-    // mode 0: e^(v - max); mode 1: the (scaled) sigmoids
+    // mode 0: e^(v - max); mode 1: the sigmoids, shifted as sigmoid_row does
     float x[NPL];
     float m = 0.f, lse = 0.f, inv = 0.f, inv_exp = 0.f, dot = 0.f;
     if constexpr (AUX) {
@@ -548,6 +552,8 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       } else {
         inv = inv_exp;
       }
+      if constexpr (kEarly)
+        if (routing && (unsigned)id[0] < (unsigned)E) lk = __ldg(a.logits + t * a.ld + id[0]);
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
         if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], x[i], dot);
@@ -575,8 +581,8 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
         gk[j] = wk[j] * (gk[j] - wg);
         if (id[j] < 0) continue;
         lost |= tag[id[j]] != lig + LPR * j + 1;
-        if constexpr (kSigmoid && !AUX)
-          gk[j] *= 1.f - sigmoid_fast(__ldg(a.logits + t * a.ld + id[j]));
+        // 1 - sigmoid of a selected expert: small as a rule, so not as a difference
+        if constexpr (kSigmoid) gk[j] *= sigmoid_fast(-(kEarly ? lk : __ldg(a.logits + t * a.ld + id[j])));
       }
       // top-K gives distinct ids: every replica found its own tag and the
       // values go out together; a repeated id adds up in k order instead
@@ -610,8 +616,9 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       if constexpr (AUX && !kSigmoid) {
         d = fmaf(x[i], fmaf(smem[c], inv, shift), d);
       } else if constexpr (AUX) {
-        // 1 - x is 1 - sigmoid for shifted rows too: 1
-        d = fmaf(x[i], fmaf(smem[c], inv, shift), d) * (1.f - x[i]);
+        // here 1 - x loses digits where x is near 1, but next to terms that do not
+        // have that small factor; the selected experts' share has it, see above
+        d = fmaf(x[i] * (1.f - x[i]), fmaf(smem[c], inv, shift), d);
         if (gz != 0.f) d = fmaf(zq, ex2((v[i] - m) * kLog2E), d);
       }
       if (RPW == 1 || in) out[c] = RPW == 1 || on ? d : 0.f;
@@ -653,12 +660,12 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
 #define MOE_TIER(f, E, LPR, NPL, ...)                                        \
   if ((E) <= LPR * NPL)                                                      \
     return (E) == LPR * NPL ? f<LPR, NPL, true>(__VA_ARGS__) : f<LPR, NPL, false>(__VA_ARGS__);
-#define MOE_BY_SHAPE(f, E, LPR128, ...)            \
+#define MOE_BY_SHAPE(f, E, LPR128, LPR256, ...)    \
   MOE_TIER(f, E, 4, 4, __VA_ARGS__)                \
   MOE_TIER(f, E, 8, 4, __VA_ARGS__)                \
   MOE_TIER(f, E, 8, 8, __VA_ARGS__)                \
   MOE_TIER(f, E, LPR128, 128 / LPR128, __VA_ARGS__) \
-  MOE_TIER(f, E, 16, 16, __VA_ARGS__)              \
+  MOE_TIER(f, E, LPR256, 256 / LPR256, __VA_ARGS__) \
   MOE_TIER(f, E, 32, 16, __VA_ARGS__)              \
   MOE_TIER(f, E, 32, 28, __VA_ARGS__)              \
   return (E) == 1024 ? f<32, 32, true>(__VA_ARGS__) : f<32, 32, false>(__VA_ARGS__);
@@ -729,7 +736,7 @@ template <int LPR, int NPL, bool FULL>
 int chunks_of_shape(int L, int n_seq) {
   return chunks_of(L, n_seq, LPR, blocks_per_sm(NPL));
 }
-int loss_chunks(int L, int n_seq, int E) { MOE_BY_SHAPE(chunks_of_shape, E, 8, L, n_seq) }
+int loss_chunks(int L, int n_seq, int E) { MOE_BY_SHAPE(chunks_of_shape, E, 8, 16, L, n_seq) }
 
 template <int LPR, int NPL, bool FULL>
 cudaError_t run_route_backward(const RouteBackwardArgs& a, cudaStream_t stream) {
@@ -768,9 +775,9 @@ cudaError_t launch_balance_loss(const float* logits, int ld, const int32_t* ids,
   }
   const BalanceArgs a{logits, ld,      ids,    mask,      T,     E,      K,         n_seq,
                       mode,   scratch, counts, mean_prob, valid, losses, dev_status};
-  MOE_BY_SHAPE(run_balance, E, 8, a, stream)
+  MOE_BY_SHAPE(run_balance, E, 8, 16, a, stream)
 }
 
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t stream) {
-  MOE_BY_SHAPE(run_route_backward, a.E, 16, a, stream)
+  MOE_BY_SHAPE(run_route_backward, a.E, 16, 32, a, stream)
 }
