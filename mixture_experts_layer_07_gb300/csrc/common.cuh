@@ -81,6 +81,21 @@ MOE_DEVICE int warp_id() { return threadIdx.x >> 5; }
 static inline size_t moe_align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 __host__ __device__ static inline int moe_cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
+// 16-byte vectors per thread for a row of H8 <= 4096 of them held by whole
+// warps: the most, up to four, that leave at most an eighth more slots empty
+// than the best choice does (few warps per row join faster; 1024 threads at
+// most).
+static inline int moe_row_vectors(int H8) {
+  int least = 0;
+  for (int v = 1; v <= 4; ++v) {
+    const int slots = moe_cdiv(H8, 32 * v) * 32 * v;
+    if (v == 1 || slots < least) least = slots;
+  }
+  for (int v = 4; v > 1; --v)
+    if (8 * moe_cdiv(H8, 32 * v) * 32 * v <= 9 * least) return v;
+  return 1;
+}
+
 // Programmatic dependent launch.  Every kernel of the layer is launched with
 // programmatic stream serialisation: the next kernel's grid may be scheduled
 // while this one runs, and each kernel waits here for its predecessor's

@@ -26,7 +26,7 @@ namespace {
 
 using namespace moe_f32x2;
 
-constexpr int kMaxWarps = 16;
+constexpr int kMaxWarps = 32;
 
 // Sum over the row's threads.  `slot` alternates between calls so that one
 // barrier per row is enough; rows of one warp need none.
@@ -39,8 +39,8 @@ MOE_DEVICE float row_sum(float v, int tpr, float (*red)[kMaxWarps], int slot) {
   __syncthreads();
   float s = lane_id() < nw ? red[slot][lane_id()] : 0.f;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return __shfl_sync(0xffffffffu, s, 0);
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
 }
 
 // largest magnitude as its bit pattern (a NaN is larger than every number, so
@@ -113,8 +113,8 @@ enum { kQNone = 0, kQGroup = 1, kQRow = 2 };
 // One row per group of tpr threads; blockDim.x / tpr rows per block (one row
 // where it takes several warps).
 // x, residual, h and y are not __restrict__: h may be x or residual, y may be x.
-template <int VPT, int MAXT, int Q, bool W32>
-__global__ void __launch_bounds__(MAXT)
+template <int VPT, int Q, bool W32>
+__global__ void __launch_bounds__(1024)
 add_rmsnorm_kernel(const uint4* x, const uint4* residual, const void* __restrict__ w, long long T,
                    int H8, float inv_h, float eps, int tpr, uint4* h_out, uint4* y,
                    float* __restrict__ rstd, uint2* __restrict__ yq, float* __restrict__ yscale) {
@@ -214,8 +214,8 @@ MOE_DEVICE void weight4(const void* w, int vec, float2* f) {
 // group late, behind the next group's sums, so that no warp waits at the
 // barrier with nothing to do.  At the end the block's rows are added and one
 // fp32 partial row is written.
-template <int VPT, int S, int MAXT, bool LAG, bool W32>
-__global__ void __launch_bounds__(MAXT, 1)
+template <int VPT, int S, int MAXT, int BPS, bool LAG, bool W32>
+__global__ void __launch_bounds__(MAXT, BPS)
 rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restrict__ h,
                         const float* __restrict__ rstd, const void* __restrict__ w, int T, int H8,
                         float inv_h, int tpr, uint4* dx, float* __restrict__ part) {
@@ -374,24 +374,22 @@ column_sum_kernel(const float* __restrict__ part, int rows, int H, float* __rest
   }
 }
 
+// Forward.  Rows of one warp go eight to a block.
 struct RowShape {
   int vpt, tpr, rpb;
 };
-
-// Up to four vectors per thread while that takes at most 256 threads (H <=
-// 8192), eight above (512 threads at H = 32768).  Rows of one warp go eight to
-// a block.
 RowShape row_shape(int H8) {
   RowShape r;
-  r.vpt = H8 <= 32 ? 1 : H8 <= 64 ? 2 : H8 <= 1024 ? 4 : 8;
+  r.vpt = moe_row_vectors(H8);
   r.tpr = moe_cdiv(H8, 32 * r.vpt) * 32;
   r.rpb = r.tpr == 32 ? 8 : 1;
   return r;
 }
 
 // Backward: one vector per thread up to 1024 threads (H <= 8192), several
-// beyond; as many rows per block as fill the threads, fewer where the rows are
-// too few to go round the SMs.  The SM count is fixed, not asked of the device:
+// beyond; two blocks of up to 512 threads per SM where a row fits one (H <=
+// 4096), else one block.  As many rows per block as fill the threads, fewer
+// where the rows are too few to go round.  The SM count is fixed, not asked of the device:
 // the scratch size must not depend on which device is current.
 constexpr int kGridSms = 152;
 struct BackShape {
@@ -401,11 +399,12 @@ BackShape back_shape(int T, int H8) {
   BackShape r;
   r.vpt = H8 <= 1024 ? 1 : H8 <= 2048 ? 4 : 8;
   r.tpr = moe_cdiv(H8, 32 * r.vpt) * 32;
-  const int share = moe_cdiv(T, kGridSms);
-  const int fit = (r.vpt == 1 ? 1024 : 512) / r.tpr;
+  const int slots = kGridSms * (H8 <= 512 ? 2 : 1);
+  const int share = moe_cdiv(T, slots);
+  const int fit = (H8 <= 512 || r.vpt > 1 ? 512 : 1024) / r.tpr;
   r.rpb = share < fit ? share : fit;
   const int groups = moe_cdiv(T, r.rpb);
-  r.grid = groups < kGridSms ? groups : kGridSms;
+  r.grid = groups < slots ? groups : slots;
   return r;
 }
 
@@ -420,28 +419,28 @@ struct NormArgs {
   float* yscale;
 };
 
-template <int VPT, int MAXT, int Q>
+template <int VPT, int Q>
 cudaError_t run_norm(bool w32, const RowShape& r, const NormArgs& a, cudaStream_t stream) {
-  auto k = w32 ? add_rmsnorm_kernel<VPT, MAXT, Q, true> : add_rmsnorm_kernel<VPT, MAXT, Q, false>;
+  auto k = w32 ? add_rmsnorm_kernel<VPT, Q, true> : add_rmsnorm_kernel<VPT, Q, false>;
   return moe_launch(k, dim3((unsigned)((a.T + r.rpb - 1) / r.rpb)), dim3(r.tpr * r.rpb), 0, stream,
                     1, static_cast<const uint4*>(a.x), static_cast<const uint4*>(a.residual), a.w,
                     a.T, a.H / 8, 1.f / (float)a.H, a.eps, r.tpr, static_cast<uint4*>(a.h),
                     static_cast<uint4*>(a.y), a.rstd, static_cast<uint2*>(a.yq), a.yscale);
 }
 
-template <int VPT, int MAXT>
+template <int VPT>
 cudaError_t run_norm_q(int q, bool w32, const RowShape& r, const NormArgs& a, cudaStream_t s) {
-  return q == kQGroup ? run_norm<VPT, MAXT, kQGroup>(w32, r, a, s)
-         : q == kQRow ? run_norm<VPT, MAXT, kQRow>(w32, r, a, s)
-                      : run_norm<VPT, MAXT, kQNone>(w32, r, a, s);
+  return q == kQGroup ? run_norm<VPT, kQGroup>(w32, r, a, s)
+         : q == kQRow ? run_norm<VPT, kQRow>(w32, r, a, s)
+                      : run_norm<VPT, kQNone>(w32, r, a, s);
 }
 
-template <int VPT, int S, int MAXT, bool LAG>
+template <int VPT, int S, int MAXT, int BPS, bool LAG>
 cudaError_t run_backward(bool w32, const BackShape& r, const void* dy, const void* dh,
                          const void* h, const float* rstd, const void* w, int T, int H, void* dx,
                          float* part, cudaStream_t stream) {
-  auto k = w32 ? rmsnorm_backward_kernel<VPT, S, MAXT, LAG, true>
-               : rmsnorm_backward_kernel<VPT, S, MAXT, LAG, false>;
+  auto k = w32 ? rmsnorm_backward_kernel<VPT, S, MAXT, BPS, LAG, true>
+               : rmsnorm_backward_kernel<VPT, S, MAXT, BPS, LAG, false>;
   constexpr size_t kPerThread = (size_t)S * 3 * VPT * 16;  // >= 32 VPT: the rows' sums fit
   static std::atomic<unsigned long long> set[2];
   cudaError_t e = moe_raise_smem(k, kPerThread * MAXT, set[w32]);
@@ -462,10 +461,10 @@ cudaError_t launch_add_rmsnorm(const void* x, const void* residual, const void* 
   const int q = !yq ? kQNone : q_group ? kQGroup : kQRow;
   const NormArgs a{x, residual, w, T, H, eps, h, y, rstd, yq, yscale};
   switch (r.vpt) {
-    case 1: return run_norm_q<1, 256>(q, w32, r, a, stream);
-    case 2: return run_norm_q<2, 256>(q, w32, r, a, stream);
-    case 4: return run_norm_q<4, 256>(q, w32, r, a, stream);
-    default: return run_norm_q<8, 512>(q, w32, r, a, stream);
+    case 1: return run_norm_q<1>(q, w32, r, a, stream);
+    case 2: return run_norm_q<2>(q, w32, r, a, stream);
+    case 3: return run_norm_q<3>(q, w32, r, a, stream);
+    default: return run_norm_q<4>(q, w32, r, a, stream);
   }
 }
 
@@ -484,10 +483,14 @@ cudaError_t launch_add_rmsnorm_backward(const void* dy, const void* dh, const vo
     const BackShape r = back_shape(T, H / 8);
     rows = r.grid;
     cudaError_t e;
-    switch (r.vpt) {  // 196 KB of ring each
-      case 1: e = run_backward<1, 4, 1024, true>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
-      case 4: e = run_backward<4, 2, 512, false>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
-      default: e = run_backward<8, 1, 512, false>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream);
+    switch (r.vpt) {  // 196 KB of ring per SM each
+      case 1:
+        e = H <= 4096
+                ? run_backward<1, 4, 512, 2, true>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream)
+                : run_backward<1, 4, 1024, 1, true>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream);
+        break;
+      case 4: e = run_backward<4, 2, 512, 1, false>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
+      default: e = run_backward<8, 1, 512, 1, false>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream);
     }
     if (e != cudaSuccess) return e;
   }

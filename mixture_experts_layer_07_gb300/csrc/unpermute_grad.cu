@@ -5,14 +5,15 @@
 //   dsh[t]       = g[t] * d          dg[t]   = <d, sh[t]>
 // One pass: a block holds d in registers (VPT 16-byte vectors per thread) and
 // walks the token's rows in groups of KB, each row read and its gradient
-// written once; the dot products of a group are reduced together.  Bound by
-// memory.  No atomics: every row belongs to one (t, k).
+// written once; the dot products of a group are reduced together.  Few tokens
+// spread their groups over gridDim.y blocks.  Bound by memory.  No atomics:
+// every row belongs to one (t, k).
 #include "common.cuh"
 #include "internal.h"
 
 namespace {
 
-constexpr int kMaxWarps = 16;
+constexpr int kMaxWarps = 32;
 
 MOE_DEVICE float dot8(const uint4& v, const float* d, float s) {
   float f[8];
@@ -29,8 +30,8 @@ MOE_DEVICE uint4 scaled8(const float* d, float w) {
 
 // Row index K of the walk stands for the shared expert's row.  y and dy (and
 // the shared pair) are not __restrict__: they may be the same buffer.
-template <int VPT, int KB, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+template <int VPT, int KB>
+__global__ void __launch_bounds__(512)
 unpermute_backward_kernel(const uint4* __restrict__ dout, const uint4* y,
                           const int32_t* __restrict__ flat_to_row,
                           const float* __restrict__ weights, int T, int K, int H8,
@@ -51,7 +52,7 @@ unpermute_backward_kernel(const uint4* __restrict__ dout, const uint4* y,
   }
   const int n = K + (d_shared_y || d_shared_gate ? 1 : 0);
   int slot = 0;
-  for (int k0 = 0; k0 < n; k0 += KB, slot ^= 1) {
+  for (int k0 = blockIdx.y * KB; k0 < n; k0 += gridDim.y * KB, slot ^= 1) {
     float acc[KB];
     long long row[KB];
     float wk[KB];
@@ -122,14 +123,17 @@ cudaError_t launch_unpermute_backward(const void* dout, const void* y, const int
                                       float* d_weights, void* d_shared_y, float* d_shared_gate,
                                       cudaStream_t stream) {
   const int H8 = H / 8;
-  const int vpt = H8 <= 64 ? 1 : H8 <= 128 ? 2 : H8 <= 1024 ? 4 : 8;
+  const int vpt = H8 <= 2048 ? moe_row_vectors(H8) : 8;  // 512 threads at most
   const int threads = moe_cdiv(H8, 32 * vpt) * 32;
-  auto k = vpt == 1   ? unpermute_backward_kernel<1, 4, 256>
-           : vpt == 2 ? unpermute_backward_kernel<2, 4, 256>
-           : vpt == 4 ? unpermute_backward_kernel<4, 4, 256>
-                      : unpermute_backward_kernel<8, 2, 512>;
+  const int kb = vpt <= 4 ? 4 : 2;
+  auto k = vpt == 1   ? unpermute_backward_kernel<1, 4>
+           : vpt == 2 ? unpermute_backward_kernel<2, 4>
+           : vpt == 3 ? unpermute_backward_kernel<3, 4>
+           : vpt == 4 ? unpermute_backward_kernel<4, 4>
+                      : unpermute_backward_kernel<8, 2>;
+  const int groups = moe_cdiv(K + (d_shared_y || d_shared_gate ? 1 : 0), kb);
   // inputs that no requested output needs are not read
-  return moe_launch(k, dim3(T), dim3(threads), 0, stream, 1, static_cast<const uint4*>(dout),
+  return moe_launch(k, dim3(T, T < 2 * 152 ? groups : 1), dim3(threads), 0, stream, 1, static_cast<const uint4*>(dout),
                     static_cast<const uint4*>(d_weights ? y : nullptr),
                     dy || d_weights ? flat_to_row : nullptr, weights, T, K, H8,
                     static_cast<const uint4*>(d_shared_gate ? shared_y : nullptr), shared_gate,
