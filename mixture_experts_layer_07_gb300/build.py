@@ -1,7 +1,8 @@
 """Build ``libmoe_gb300.so`` in-tree for sm_103a with nvcc.
 
 Each ``csrc/*.cu`` is compiled to an object in parallel, then linked into a
-shared library next to this file.  Objects are rebuilt only when a source or
+shared library next to this file, and ``csrc/binding.cpp`` into the Python
+module ``_moe_binding`` beside it.  Objects are rebuilt only when a source or
 header is newer.  Usage: ``python -m mixture_experts_layer_07_gb300.build``.
 """
 from __future__ import annotations
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
+BINDING = os.path.join(PKG, "_moe_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -71,9 +74,20 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr, flush=True)
 
+    # the Python module: host code, compiled along with the kernels
+    src = os.path.join(CSRC, "binding.cpp")
+    bind = None
+    if _stale(BINDING, [src] + headers):
+        bind = [cc, "-O2", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-cudart", "none", "-I",
+                INCLUDE, "-I", sysconfig.get_paths()["include"], src, "-o", BINDING + ".tmp"]
+        jobs.append(bind)
+
     if jobs:
         with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             list(ex.map(run, jobs))
+    if bind:
+        os.replace(BINDING + ".tmp", BINDING)
+        jobs.remove(bind)
     if jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp"
         run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])

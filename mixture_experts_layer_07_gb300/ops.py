@@ -1,4 +1,5 @@
-"""ctypes binding of ``libmoe_gb300.so`` -- argument marshalling only.
+"""Binding of ``libmoe_gb300.so`` -- argument marshalling only: ctypes, and for the operators
+around the layer (norm, router losses, gradients) the C module ``_moe_binding``.
 
 Each function has the name of the C entry point it calls (without the
 ``moe_`` prefix), passes tensor data pointers and the current CUDA stream, and
@@ -15,6 +16,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_gb300.so")
+BINDING_PATH = os.path.join(_HERE, "_moe_binding.so")
 
 MODE_SOFTMAX, MODE_SIGMOID_BIAS = 0, 1
 W_BF16, W_FP8, W_MXFP4, W8A8_FP8 = 0, 1, 2, 3
@@ -71,14 +73,15 @@ class WorkspaceLayout(ctypes.Structure):
 
 
 _L = None
+_B = None  # _moe_binding, once the library is loaded
 _P, _I, _F, _S, _I64 = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t,
                         ctypes.c_int64)
 
 
 def _lib():
-    global _L
+    global _L, _B
     if _L is None:
-        if not os.path.exists(LIB_PATH):
+        if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
             raise RuntimeError(f"{LIB_PATH} is not built: run __graft_entry__.build() "
                                "(the MoE path has no fallback)")
         lib = ctypes.CDLL(LIB_PATH)
@@ -122,7 +125,11 @@ def _lib():
             fn = getattr(lib, name)
             fn.restype = _I
             fn.argtypes = args
-        _L = lib
+        from . import _moe_binding
+        _moe_binding.connect(*[ctypes.cast(getattr(lib, "moe_" + n), _P).value for n in
+                               ("add_rmsnorm", "add_rmsnorm_backward", "balance_loss",
+                                "route_backward", "unpermute_backward")])
+        _L, _B = lib, _moe_binding
     return _L
 
 
@@ -272,44 +279,18 @@ def unpermute(y, flat_to_row, weights, T, K, H, out, shared_y=None, shared_gate=
                                 _p(shared_gate), _p(out), _stream(stream)), "moe_unpermute")
 
 
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
-_MASK = (torch.uint8, torch.bool)
-_E4M3 = (torch.float8_e4m3fn, torch.uint8)  # codes, as either
-
-
-def _pc(t, dtype, numel, name):
-    """Device pointer of a tensor (or None) that must hold `numel` values of `dtype` (or of one
-    of several)."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.numel() == numel and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
-        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
-    if t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor of {numel} values expected, got shape "
-                         f"{tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _norm_weight(weight, H):
-    f32 = weight.dtype == _F32
-    return _pc(weight, _F32 if f32 else _BF16, H, "weight"), DT_F32 if f32 else DT_BF16
+def _bind():
+    if _B is None:
+        _lib()
+    return _B
 
 
 def add_rmsnorm(x, weight, eps, y, *, residual=None, h=None, rstd=None, yq=None, yq_scale=None,
                 q_group=128, stream=None):
     """y = rmsnorm(x + residual) * weight, h = x + residual; yq / yq_scale: y as e4m3 codes with
     a scale per 128 columns (q_group 128) or per row (q_group 0)."""
-    T, H = x.shape
-    w, wdt = _norm_weight(weight, H)
-    n = T * H
-    _check(_lib().moe_add_rmsnorm(
-        _pc(x, _BF16, n, "x"), _pc(residual, _BF16, n, "residual"), w, wdt, T, H, eps,
-        _pc(h, _BF16, n, "h"), _pc(y, _BF16, n, "y"), _pc(rstd, _F32, T, "rstd"),
-        _pc(yq, _E4M3, n, "yq"),
-        _pc(yq_scale, _F32, T * (-(-H // 128) if q_group else 1), "yq_scale"), q_group,
-        _stream(stream)), "moe_add_rmsnorm")
+    _check(_bind().add_rmsnorm(x, weight, eps, y, residual, h, rstd, yq, yq_scale, q_group, stream),
+           "moe_add_rmsnorm")
 
 
 def add_rmsnorm_backward_scratch_bytes(T: int, H: int) -> int:
@@ -320,14 +301,9 @@ def add_rmsnorm_backward_scratch_bytes(T: int, H: int) -> int:
 
 
 def add_rmsnorm_backward(dy, h, rstd, weight, dx, dweight, scratch, *, dh=None, stream=None):
-    T, H = h.shape
-    w, wdt = _norm_weight(weight, H)
-    n = T * H
-    _check(_lib().moe_add_rmsnorm_backward(
-        _pc(dy, _BF16, n, "dy"), _pc(dh, _BF16, n, "dh"), _pc(h, _BF16, n, "h"),
-        _pc(rstd, _F32, T, "rstd"), w, wdt, T, H, _pc(dx, _BF16, n, "dx"),
-        _pc(dweight, _F32, H, "dweight"), _p(scratch), scratch.numel() * scratch.element_size(),
-        _stream(stream)), "moe_add_rmsnorm_backward")
+    """dx (of x and the residual alike) and dweight [H] fp32; scratch: uint8."""
+    _check(_bind().add_rmsnorm_backward(dy, h, rstd, weight, dx, dweight, scratch, dh, stream),
+           "moe_add_rmsnorm_backward")
 
 
 def balance_loss_scratch_bytes(T: int, E: int, n_seq: int = 1) -> int:
@@ -340,16 +316,9 @@ def balance_loss_scratch_bytes(T: int, E: int, n_seq: int = 1) -> int:
 def balance_loss(logits, ids, E, counts, mean_prob, valid, losses, scratch, *, n_seq=1,
                  mode=MODE_SOFTMAX, token_mask=None, dev_status=None, stream=None):
     """counts, mean_prob [n_seq, E], valid [n_seq + 2] and losses [2] (load balance, router z) of
-    a routed batch; see the header."""
-    T, ld = logits.shape
-    K = ids.shape[1]
-    _check(_lib().moe_balance_loss(
-        _pc(logits, _F32, T * ld, "logits"), ld, _pc(ids, _I32, T * K, "ids"),
-        _pc(token_mask, _MASK, T, "token_mask"), T, E, K, n_seq, mode,
-        _pc(counts, _I32, n_seq * E, "counts"), _pc(mean_prob, _F32, n_seq * E, "mean_prob"),
-        _pc(valid, _I32, n_seq + 2, "valid"), _pc(losses, _F32, 2, "losses"), _p(scratch),
-        scratch.numel() * scratch.element_size(), _p(dev_status), _stream(stream)),
-        "moe_balance_loss")
+    a routed batch; scratch: uint8, zero before its first use; see the header."""
+    _check(_bind().balance_loss(logits, ids, E, counts, mean_prob, valid, losses, scratch, n_seq,
+                                mode, token_mask, dev_status, stream), "moe_balance_loss")
 
 
 def route_backward(logits, ids, E, dlogits, *, mode=MODE_SOFTMAX, scale=1.0, weights=None,
@@ -357,29 +326,18 @@ def route_backward(logits, ids, E, dlogits, *, mode=MODE_SOFTMAX, scale=1.0, wei
                    valid=None, grad_losses=None, dev_status=None, stream=None):
     """dlogits from the gradients of the routing weights, the shared gate and balance_loss's two
     losses; see the header."""
-    T, ld = logits.shape
-    K, ldd = ids.shape[1], dlogits.shape[1]
-    _check(_lib().moe_route_backward(
-        _pc(logits, _F32, T * ld, "logits"), ld, _pc(ids, _I32, T * K, "ids"),
-        _pc(weights, _F32, T * K, "weights"), _pc(d_weights, _F32, T * K, "d_weights"),
-        _pc(d_shared_gate, _F32, T, "d_shared_gate"), _pc(token_mask, _MASK, T, "token_mask"), T,
-        E, K, n_seq, mode, scale, _pc(counts, _I32, n_seq * E, "counts"),
-        _pc(valid, _I32, n_seq + 2, "valid"), _pc(grad_losses, _F32, 2, "grad_losses"),
-        _pc(dlogits, _F32, T * ldd, "dlogits"), ldd, _p(dev_status), _stream(stream)),
-        "moe_route_backward")
+    _check(_bind().route_backward(logits, ids, E, dlogits, mode, scale, weights, d_weights,
+                                  d_shared_gate, token_mask, n_seq, counts, valid, grad_losses,
+                                  dev_status, stream), "moe_route_backward")
 
 
 def unpermute_backward(dout, flat_to_row, weights, T, K, H, *, y=None, dy=None, d_weights=None,
                        shared_y=None, shared_gate=None, d_shared_y=None, d_shared_gate=None,
                        stream=None):
-    n, r = T * H, T * K * H
-    _check(_lib().moe_unpermute_backward(
-        _pc(dout, _BF16, n, "dout"), _pc(y, _BF16, r, "y"),
-        _pc(flat_to_row, _I32, T * K, "flat_to_row"), _pc(weights, _F32, T * K, "weights"), T, K,
-        H, _pc(shared_y, _BF16, n, "shared_y"), _pc(shared_gate, _F32, T, "shared_gate"),
-        _pc(dy, _BF16, r, "dy"), _pc(d_weights, _F32, T * K, "d_weights"),
-        _pc(d_shared_y, _BF16, n, "d_shared_y"), _pc(d_shared_gate, _F32, T, "d_shared_gate"),
-        _stream(stream)), "moe_unpermute_backward")
+    """Gradients of unpermute: dy, d_weights, d_shared_y, d_shared_gate, each where given."""
+    _check(_bind().unpermute_backward(dout, flat_to_row, weights, T, K, H, y, dy, d_weights,
+                                      shared_y, shared_gate, d_shared_y, d_shared_gate, stream),
+           "moe_unpermute_backward")
 
 
 def layer(cfg: Config, x, weights: Weights, out, workspace, dev_status=None, stream=None, T=None):
@@ -392,13 +350,10 @@ def layer(cfg: Config, x, weights: Weights, out, workspace, dev_status=None, str
 def layer_q8(cfg: Config, x, xq, xq_scale, weights: Weights, out, workspace, dev_status=None,
              stream=None):
     """moe_layer on activations that are e4m3 codes already (W8A8 experts; see the header)."""
-    T, H = x.shape
-    _check(_lib().moe_layer_q8(ctypes.byref(cfg), T, _pc(x, _BF16, T * cfg.H, "x"),
-                               _pc(xq, _E4M3, T * cfg.H, "xq"),
-                               _pc(xq_scale, _F32, T * -(-cfg.H // 128), "xq_scale"),
-                               ctypes.byref(weights), _pc(out, _BF16, T * cfg.H, "out"),
-                               _p(workspace), workspace.numel(), _p(dev_status),
-                               _stream(stream)), "moe_layer_q8")
+    T = x.shape[0]
+    _check(_lib().moe_layer_q8(ctypes.byref(cfg), T, _p(x), _p(xq), _p(xq_scale),
+                               ctypes.byref(weights), _p(out), _p(workspace), workspace.numel(),
+                               _p(dev_status), _stream(stream)), "moe_layer_q8")
 
 
 class MoELayer:

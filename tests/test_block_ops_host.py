@@ -131,3 +131,16 @@ def test_binding_refuses_other_types_shapes_and_strides(ops):
     with pytest.raises(ValueError, match="dy"):
         ops.unpermute_backward(x, torch.zeros(8, dtype=i32), torch.zeros(4, 2), 4, 2, 64,
                                dy=torch.zeros(4, 64, dtype=bf))
+
+
+def test_binding_refuses_tensors_of_the_host(ops):
+    bf = torch.bfloat16
+    x, w = torch.zeros(4, 64, dtype=bf), torch.ones(64, dtype=bf)
+    with pytest.raises(ValueError, match="x: a tensor on the GPU"):
+        ops.add_rmsnorm(x, w, 1e-6, torch.zeros(4, 64, dtype=bf))
+    with pytest.raises(ValueError, match="x: a matrix"):
+        ops.add_rmsnorm(x[0], w, 1e-6, x)
+    with pytest.raises(TypeError):
+        ops.add_rmsnorm(x, w, "eps", x)
+    with pytest.raises(AttributeError):
+        ops.add_rmsnorm([1.0], w, 1e-6, x)
