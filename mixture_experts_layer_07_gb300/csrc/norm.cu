@@ -15,6 +15,10 @@
 // threads (a multiple of the warp), each owning the 16-byte vectors
 // tid + tpr*j, j < VPT; a 128-column scale group is then the 16 vectors of half
 // a warp, so its maximum needs four shuffles.
+// Measured on one GB300 (copy rate 6778 GB/s): T = 8191, H = 7168 with residual
+// and a scale per row 79.8 us, 98 % of the copy rate; T = 4096, H = 2880 with a
+// scale per 128 columns 20.3 us (77 %, 2.3 us of it the launch); T = 1, H = 2048
+// 2.3 us.  Backward T = 8192, H = 7168 77.6 us (89 %).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -213,7 +217,9 @@ MOE_DEVICE void weight4(const void* w, int vec, float2* f) {
 // products take one barrier per group.  With LAG, a group's dx is computed one
 // group late, behind the next group's sums, so that no warp waits at the
 // barrier with nothing to do.  At the end the block's rows are added and one
-// fp32 partial row is written.
+// fp32 partial row is written.  (T = 8192, H = 7168: rows loaded into registers
+// when their turn comes 88 us; ring of two stages, two vectors per thread 86;
+// four stages, one vector, LAG 78.)
 template <int VPT, int S, int MAXT, int BPS, bool LAG, bool W32>
 __global__ void __launch_bounds__(MAXT, BPS)
 rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restrict__ h,

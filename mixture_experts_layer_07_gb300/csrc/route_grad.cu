@@ -19,8 +19,14 @@
 // sigmoid) in mode 1]: mode 0 is softmax over the selected logits (scale 1),
 // mode 1 is scale * sigmoid / sum of the selected sigmoids.
 //
-// Memory bounds both: each row of logits is read once into registers (a group
-// of LPR lanes per row, NPL columns per lane) and used for every sum.
+// Memory bounds both where the batch is large: each row of logits is read once
+// into registers (a group of LPR lanes per row, NPL columns per lane, the next
+// row on its way) and used for every sum.  Measured on one GB300: losses T = 8 x
+// 4096, E = 512, half padded 13.6 us; losses and gradient T = 4 x 2048, E = 896,
+// sigmoid, padded 23.4 us; T = 65536, E = 512 losses 29 us (70 % of the copy
+// rate; 8 us of it are the launch and the hand-over between blocks, the marginal
+// rate is 95 %), gradient 54 us (75 %).  Small batches are bound by latency:
+// T = 2048, E = 128 losses 4.3 us.
 // Determinism: a block's probability sums are fp32 in a fixed order; across
 // blocks they are added as 64-bit fixed point, so the order does not matter.
 #include "common.cuh"
@@ -187,10 +193,10 @@ constexpr int back_blocks_per_sm(int lpr, int npl) {
 // ---------------------------------------------------------------- forward
 // Block b takes every chunks-th pass of kStep rows of sequence b / chunks, from
 // pass b % chunks on, so that padding at a sequence's end is spread over its
-// blocks.  The last block of a
-// sequence to finish turns its sums into outputs, and the last sequence's
-// block the sequences' losses into the batch's.  A sequence of one block, and
-// a batch of one sequence, skip the hand-over through global memory.
+// blocks.  The last block of a sequence to finish turns its sums into outputs,
+// and the last sequence's block the sequences' losses into the batch's.  A
+// sequence of one block, and a batch of one sequence, skip the hand-over
+// through global memory.
 template <int LPR, int NPL, int MODE, bool FULL>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(NPL))
 balance_kernel(const float* __restrict__ logits, int ld, const int32_t* __restrict__ ids,
