@@ -145,6 +145,26 @@ def test_norm_in_place_and_single_outputs(ops):
     assert torch.equal(yq, ref["yq"].view(torch.uint8)) and torch.equal(ys, ref["yq_scale"])
 
 
+@pytest.mark.parametrize("magnitude", [1.0, 1e-30, 1e28])
+@pytest.mark.parametrize("q", [128, 0])
+def test_norm_codes_are_those_of_ieee_division(ops, magnitude, q):
+    # the kernel's own fp32 operations, one by one: y = (h s) w, scale = amax / 448, y / scale
+    T, H = 67, 2000
+    x, r, w = norm_inputs(T, H, True, 21, torch.float32)
+    w = w * magnitude  # scales far outside 2^+-80 take the division itself
+    o = run_norm(ops, x, r, w, q)
+    y = ((x.float() + r.float()) * o["rstd"][:, None]) * w
+    group = q or H
+    n = -(-H // group)
+    p = torch.zeros(T, n * group, device="cuda")
+    p[:, :H] = y
+    m = p.view(T, n, group).abs().amax(2)
+    scale = m / torch.full_like(m, 448.0)
+    assert torch.equal(o["yq_scale"], scale)
+    code = (p.view(T, n, group) / scale[..., None].expand(T, n, group)).view(T, n * group)[:, :H]
+    assert torch.equal(o["yq"].view(torch.uint8), code.to(torch.float8_e4m3fn).view(torch.uint8))
+
+
 @pytest.mark.parametrize("T,H", SIZES)
 @pytest.mark.parametrize("with_dh", [False, True])
 def test_norm_backward_matches_oracle(ops, T, H, with_dh):
