@@ -32,16 +32,47 @@ using namespace moe_f32x2;
 
 constexpr int kMaxWarps = 32;
 
-// Sum over the row's threads.  `slot` alternates between calls so that one
-// barrier per row is enough; rows of one warp need none.
-MOE_DEVICE float row_sum(float v, int tpr, float (*red)[kMaxWarps], int slot) {
+// Sum of v over the row, in an order that depends on H alone, not on how the
+// row is spread over threads (nor so on the batch): first the 32 vectors of a
+// chunk, lanes 16 apart, 8 apart and so on, then the chunks likewise, chunk i at
+// lane i % 32.  A warp's VPT chunks are halved as the distance is -- a lane hands
+// over what its partner goes on with -- so four take six exchanges, not twenty.
+template <int VPT>
+MOE_DEVICE float row_sum(const float (&v)[VPT], int tpr, float* red) {
+  const int lane = lane_id();
+  float s = v[0];
+  int mine = 0;  // the chunk whose sum this lane ends up with
+  if constexpr (VPT == 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+  } else if constexpr (VPT == 2) {
+    mine = lane >> 4;
+    s = mine ? v[1] : v[0];
+    s += __shfl_xor_sync(0xffffffffu, mine ? v[0] : v[1], 16);
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+  } else {
+    const float v3 = VPT == 4 ? v[VPT - 1] : 0.f;
+    const bool hi = lane & 16, odd = lane & 8;
+    float a = hi ? v[2] : v[0], b = hi ? v3 : v[1];
+    a += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+    b += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v3, 16);
+    s = odd ? b : a;
+    s += __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+    mine = 2 * (lane >> 4) + (lane >> 3 & 1);  // 0, 1, 2, 3 from lanes 0, 8, 16, 24
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (tpr == 32) return v;
+  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (tpr == 32) {  // the chunks' sum as the butterfly below makes it
+    if constexpr (VPT > 1) s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if constexpr (VPT > 2) s += __shfl_xor_sync(0xffffffffu, s, 8);
+    return s;
+  }
   const int nw = tpr >> 5;  // a row of several warps is the whole block
-  if (lane_id() == 0) red[slot][warp_id()] = v;
+  constexpr int kEach = VPT == 1 ? 32 : VPT == 2 ? 16 : 8;  // lanes per chunk
+  if (lane % kEach == 0 && mine < VPT) red[warp_id() + nw * mine] = s;
   __syncthreads();
-  float s = lane_id() < nw ? red[slot][lane_id()] : 0.f;
+  s = 0.f;
+  for (int i = lane; i < nw * VPT; i += 32) s += red[i];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
@@ -122,7 +153,7 @@ __global__ void __launch_bounds__(1024)
 add_rmsnorm_kernel(const uint4* x, const uint4* residual, const void* __restrict__ w, long long T,
                    int H8, float inv_h, float eps, int tpr, uint4* h_out, uint4* y,
                    float* __restrict__ rstd, uint2* __restrict__ yq, float* __restrict__ yscale) {
-  __shared__ float red[2][kMaxWarps];
+  __shared__ float red[4 * kMaxWarps];
   __shared__ uint32_t redm[kMaxWarps];
   pdl_wait();
   pdl_trigger();
@@ -140,21 +171,22 @@ add_rmsnorm_kernel(const uint4* x, const uint4* residual, const void* __restrict
     b[j] = in && residual ? residual[base + c] : make_uint4(0u, 0u, 0u, 0u);
   }
   float h[VPT][8];
-  float ss = 0.f;
+  float ss[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     float r[8];
+    ss[j] = 0.f;
     bf16x8_to_f32(a[j], h[j]);
     bf16x8_to_f32(b[j], r);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       h[j][q] += r[q];
-      ss = fmaf(h[j][q], h[j][q], ss);
+      ss[j] = fmaf(h[j][q], h[j][q], ss[j]);
     }
     const int c = lt + tpr * j;
     if (h_out && c < H8) h_out[base + c] = pack8(h[j]);
   }
-  const float s = __frsqrt_rn(fmaf(row_sum(ss, tpr, red, 0), inv_h, eps));
+  const float s = __frsqrt_rn(fmaf(row_sum(ss, tpr, red), inv_h, eps));
   if (rstd && lt == 0) rstd[t] = s;
   uint32_t m = 0;
 #pragma unroll
@@ -380,13 +412,18 @@ column_sum_kernel(const float* __restrict__ part, int rows, int H, float* __rest
   }
 }
 
-// Forward.  Rows of one warp go eight to a block.
+// Forward.  Where the rows are too few to fill the SMs the call is one row's
+// latency, and as many threads as a row can feed shorten it (T = 1, H = 2048 2.4
+// -> 1.7 us against the four vectors per thread that large batches take; T =
+// 8191, H = 7168 79.8 -> 99.5 us the other way).  Rows of one warp go eight to a
+// block.
+constexpr int kGridSms = 152;
 struct RowShape {
   int vpt, tpr, rpb;
 };
-RowShape row_shape(int H8) {
+RowShape row_shape(long long T, int H8) {
   RowShape r;
-  r.vpt = moe_row_vectors(H8);
+  r.vpt = T >= 2 * kGridSms ? moe_row_vectors(H8) : H8 <= 1024 ? 1 : H8 <= 2048 ? 2 : 4;
   r.tpr = moe_cdiv(H8, 32 * r.vpt) * 32;
   r.rpb = r.tpr == 32 ? 8 : 1;
   return r;
@@ -397,7 +434,6 @@ RowShape row_shape(int H8) {
 // 4096), else one block.  As many rows per block as fill the threads, fewer
 // where the rows are too few to go round.  The SM count is fixed, not asked of the device:
 // the scratch size must not depend on which device is current.
-constexpr int kGridSms = 152;
 struct BackShape {
   int vpt, tpr, rpb, grid;
 };
@@ -463,7 +499,7 @@ cudaError_t run_backward(bool w32, const BackShape& r, const void* dy, const voi
 cudaError_t launch_add_rmsnorm(const void* x, const void* residual, const void* w, bool w32, int T,
                                int H, float eps, void* h, void* y, float* rstd, void* yq,
                                float* yscale, int q_group, cudaStream_t stream) {
-  const RowShape r = row_shape(H / 8);
+  const RowShape r = row_shape(T, H / 8);
   const int q = !yq ? kQNone : q_group ? kQGroup : kQRow;
   const NormArgs a{x, residual, w, T, H, eps, h, y, rstd, yq, yscale};
   switch (r.vpt) {

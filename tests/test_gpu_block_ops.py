@@ -165,6 +165,17 @@ def test_norm_codes_are_those_of_ieee_division(ops, magnitude, q):
     assert torch.equal(o["yq"].view(torch.uint8), code.to(torch.float8_e4m3fn).view(torch.uint8))
 
 
+@pytest.mark.parametrize("H", [256, 272, 528, 1040, 2048, 2880, 8192, 8208, 16400, 32768])
+def test_norm_of_a_row_does_not_depend_on_the_batch(ops, H):
+    x, r, w = norm_inputs(400, H, True, H)
+    whole = run_norm(ops, x, r, w, 128)
+    for a, b in ((0, 1), (17, 20), (100, 400)):
+        part = run_norm(ops, x[a:b].contiguous(), r[a:b].contiguous(), w, 128)
+        for k in ("y", "h", "rstd", "yq_scale"):
+            assert torch.equal(part[k], whole[k][a:b]), k
+        assert torch.equal(part["yq"].view(torch.uint8), whole["yq"][a:b].view(torch.uint8))
+
+
 @pytest.mark.parametrize("T,H", SIZES)
 @pytest.mark.parametrize("with_dh", [False, True])
 def test_norm_backward_matches_oracle(ops, T, H, with_dh):
