@@ -266,26 +266,32 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restric
   const int groups = (T + rpb - 1) / rpb;
   pdl_wait();
   pdl_trigger();
-  auto slot_of = [&](int st, int arr, int j) { return ring + ((st * 3 + arr) * VPT + j) * nt + threadIdx.x; };
-  auto issue = [&](int g, int st) {
-    const long long t = (long long)g * rpb + rs;
-    if (g < groups && t < T) {
+  // vector j of array arr (dy, h, dh) in stage st
+  const int arrs = VPT * nt;
+  auto slot_of = [&](int st, int arr, int j) { return ring + (st * 3 + arr) * arrs + j * nt + threadIdx.x; };
+  // this thread's first vector of the group that is issued, and of the one that
+  // is finished; groups lie `step` apart
+  const int step = gridDim.x;
+  const size_t hop = (size_t)step * rpb * H8;
+  const uint32_t rows = (uint32_t)step * rpb;
+  uint32_t t_issue = blockIdx.x * rpb + rs, t_done = t_issue;  // rows; past T: nothing to do
+  size_t o_issue = (size_t)t_issue * H8 + lt, o_done = o_issue;
+  auto issue = [&](int st) {
+    if (t_issue < (uint32_t)T) {
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int c = lt + tpr * j;
-        if (c >= H8) continue;
-        const size_t o = (size_t)t * H8 + c;
+        if (lt + tpr * j >= H8) continue;
+        const size_t o = o_issue + tpr * j;
         moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 0, j)), dy + o, 16);
         moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 1, j)), h + o, 16);
         if (dh) moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 2, j)), dh + o, 16);
       }
     }
     moe_ptx::cp_async_commit();
+    t_issue += rows;
+    o_issue += hop;
   };
-  auto row_rstd = [&](int g) {
-    const long long t = (long long)g * rpb + rs;
-    return g < groups && t < T ? __ldg(rstd + t) : 0.f;
-  };
+  auto row_rstd = [&](uint32_t t) { return t < (uint32_t)T ? __ldg(rstd + t) : 0.f; };
   constexpr bool kKeepW = VPT == 1;  // the weight stays in registers where they suffice
   float2 dw[VPT][4], wk[4];
 #pragma unroll
@@ -294,9 +300,9 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restric
     for (int q = 0; q < 4; ++q) dw[j][q] = pair(0.f);
   if (kKeepW && lt < H8) weight4<W32>(w, lt, wk);
 
-  // dx of group g, whose rows lie in stage st and whose dot products in red[slot]
-  auto finish = [&](int g, int st, int slot, float s, float dot) {
-    const long long t = (long long)g * rpb + rs;
+  // dx of the next group to finish, whose rows lie in stage st and whose dot
+  // products in red[slot]
+  auto finish = [&](int st, int slot, float s, float dot) {
     if (wpr > 1) {
       dot = lane_id() < wpr ? red[slot][rs * wpr + lane_id()] : 0.f;
 #pragma unroll
@@ -305,34 +311,34 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restric
     const float c1 = -(dot * inv_h) * s;  // dx = s (dy w + h c1) + dh
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int c = lt + tpr * j;
-      if (c >= H8 || t >= T) continue;
+      if (lt + tpr * j >= H8 || t_done >= (uint32_t)T) continue;
       float2 gf[4], hf[4], wf[4], ef[4], o[4];
       unpack4(*slot_of(st, 0, j), gf);
       unpack4(*slot_of(st, 1, j), hf);
       unpack4(dh ? *slot_of(st, 2, j) : make_uint4(0u, 0u, 0u, 0u), ef);
-      if constexpr (!kKeepW) weight4<W32>(w, c, wf);
+      if constexpr (!kKeepW) weight4<W32>(w, lt + tpr * j, wf);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         o[q] = fma2(pair(s), fma2(hf[q], pair(c1), mul2(gf[q], kKeepW ? wk[q] : wf[q])), ef[q]);
-      dx[(size_t)t * H8 + c] = make_uint4(pack_bf16x2(o[0].x, o[0].y), pack_bf16x2(o[1].x, o[1].y),
-                                          pack_bf16x2(o[2].x, o[2].y), pack_bf16x2(o[3].x, o[3].y));
+      dx[o_done + tpr * j] = make_uint4(pack_bf16x2(o[0].x, o[0].y), pack_bf16x2(o[1].x, o[1].y),
+                                        pack_bf16x2(o[2].x, o[2].y), pack_bf16x2(o[3].x, o[3].y));
     }
+    t_done += rows;
+    o_done += hop;
   };
 
-  int g = blockIdx.x;
-  const int step = gridDim.x;
+  uint32_t t = t_issue;  // the current group's row
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) issue(g + i * step, i);
-  float s = row_rstd(g), s_prev = 0.f, dot_prev = 0.f;
+  for (int i = 0; i < kAhead; ++i) issue(i);
+  float s = row_rstd(t), s_prev = 0.f, dot_prev = 0.f;
   int it = 0;
-  for (; g < groups; ++it, g += step) {
-    issue(g + kAhead * step, (it + kAhead) % S);
-    const float s_next = row_rstd(g + step);
+  for (int g = blockIdx.x; g < groups; ++it, g += step) {
+    issue((it + kAhead) % S);
+    const float s_next = row_rstd(t + rows);
     moe_ptx::cp_async_wait<kAhead>();
     const int st = it % S;
     float2 dot2 = pair(0.f);
-    if ((long long)g * rpb + rs < T) {
+    if (t < (uint32_t)T) {
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         if (lt + tpr * j >= H8) continue;
@@ -352,14 +358,15 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restric
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if (wpr > 1 && lane_id() == 0) red[it & 1][warp_id()] = dot;
-    if (LAG && it > 0) finish(g - step, (it - 1) % S, (it - 1) & 1, s_prev, dot_prev);
+    if (LAG && it > 0) finish((it - 1) % S, (it - 1) & 1, s_prev, dot_prev);
     if (wpr > 1) __syncthreads();
-    if (!LAG) finish(g, st, it & 1, s, dot);
+    if (!LAG) finish(st, it & 1, s, dot);
     s_prev = s;
     dot_prev = dot;
     s = s_next;
+    t += rows;
   }
-  if (LAG && it > 0) finish(g - step, (it - 1) % S, (it - 1) & 1, s_prev, dot_prev);
+  if (LAG && it > 0) finish((it - 1) % S, (it - 1) & 1, s_prev, dot_prev);
 
   float4* p = reinterpret_cast<float4*>(part) + (size_t)blockIdx.x * H8 * 2;
   // one row per block: its sums are the block's; else they meet in the ring,
