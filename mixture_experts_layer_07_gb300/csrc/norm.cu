@@ -71,8 +71,12 @@ MOE_DEVICE float row_sum(const float (&v)[VPT], int tpr, float* red) {
   constexpr int kEach = VPT == 1 ? 32 : VPT == 2 ? 16 : 8;  // lanes per chunk
   if (lane % kEach == 0 && mine < VPT) red[warp_id() + nw * mine] = s;
   __syncthreads();
-  s = 0.f;
-  for (int i = lane; i < nw * VPT; i += 32) s += red[i];
+  const int n = nw * VPT;
+  s = lane < n ? red[lane] : 0.f;
+  if (n > 32) {
+#pragma unroll
+    for (int i = 32; i < 4 * kMaxWarps; i += 32) s += lane + i < n ? red[lane + i] : 0.f;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
