@@ -17,8 +17,8 @@
 // a warp, so its maximum needs four shuffles.
 // Measured on one GB300 (copy rate 6778 GB/s): T = 8191, H = 7168 with residual
 // and a scale per row 79.8 us, 98 % of the copy rate; T = 4096, H = 2880 with a
-// scale per 128 columns 20.3 us (77 %, 2.3 us of it the launch); T = 1, H = 2048
-// 2.3 us.  Backward T = 8192, H = 7168 77.6 us (89 %).
+// scale per 128 columns 20.9 us (75 %, 1.7 us of it the launch); T = 1, H = 2048
+// 1.7 us.  Backward T = 8192, H = 7168 75.8 us (91 %).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -255,7 +255,7 @@ MOE_DEVICE void weight4(const void* w, int vec, float2* f) {
 // barrier with nothing to do.  At the end the block's rows are added and one
 // fp32 partial row is written.  (T = 8192, H = 7168: rows loaded into registers
 // when their turn comes 88 us; ring of two stages, two vectors per thread 86;
-// four stages, one vector, LAG 78.)
+// four stages, one vector, LAG 78; running offsets 76.)
 template <int VPT, int S, int MAXT, int BPS, bool LAG, bool W32>
 __global__ void __launch_bounds__(MAXT, BPS)
 rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restrict__ h,
