@@ -351,6 +351,10 @@ def layer_q8(cfg: Config, x, xq, xq_scale, weights: Weights, out, workspace, dev
              stream=None):
     """moe_layer on activations that are e4m3 codes already (W8A8 experts; see the header)."""
     T = x.shape[0]
+    for t, n, name in ((x, T * cfg.H, "x"), (xq, T * cfg.H, "xq"),
+                       (xq_scale, T * -(-cfg.H // 128), "xq_scale"), (out, T * cfg.H, "out")):
+        if t.numel() != n:
+            raise ValueError(f"{name}: {n} values expected, got shape {tuple(t.shape)}")
     _check(_lib().moe_layer_q8(ctypes.byref(cfg), T, _p(x), _p(xq), _p(xq_scale),
                                ctypes.byref(weights), _p(out), _p(workspace), workspace.numel(),
                                _p(dev_status), _stream(stream)), "moe_layer_q8")

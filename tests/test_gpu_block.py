@@ -39,6 +39,15 @@ def test_layer_q8_refusals(ops):
     assert f(cfg, n=ops.workspace_bytes(cfg) - 1) == 3
 
 
+def test_layer_q8_refuses_other_sizes(ops):
+    cfg = ops.make_config(64, 256, 8, 2, 128, wdtype=ops.W8A8_FP8)
+    x, q, s = torch.zeros(4, 256), torch.zeros(4, 256, dtype=torch.uint8), torch.zeros(4, 2)
+    for args, name in (((x[:, :128], q, s, x), "x"), ((x, q[:3], s, x), "xq"), ((x, q, s[:, :1], x), "xq_scale"),
+                       ((x, q, s, x[:2]), "out")):
+        with pytest.raises(ValueError, match=f"^{name}: "):
+            ops.layer_q8(cfg, args[0], args[1], args[2], None, args[3], None)
+
+
 def quantise(y):
     """Codes and scales per row and 128 columns, as the W8A8 path quantises bf16 rows."""
     T, H = y.shape
