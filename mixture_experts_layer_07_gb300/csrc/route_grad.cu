@@ -676,9 +676,11 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
   MOE_TIER(f, E, 32, 28, __VA_ARGS__)              \
   return (E) == 1024 ? f<32, 32, true>(__VA_ARGS__) : f<32, 32, false>(__VA_ARGS__);
 
-// One wave of blocks over all sequences, at least one pass of the block's
-// warps each; a fixed SM count, so that the scratch size does not depend on
-// which device is current.
+// `blocks` per SM over all sequences, at least one pass of the block's warps
+// each; a fixed SM count, so that the scratch size does not depend on which
+// device is current.  (Losses: one wave.  Their blocks add to the same E sums,
+// so twice as many cost T = 32768, E = 512 18.6 -> 22.5 us; a third as many of 24
+// warps gained nothing there and lost 3 us on padded batches.)
 constexpr int kGridSms = 152;
 int chunks_of(int L, int n_seq, int lpr, int blocks) {
   const int passes = moe_cdiv(L, kWarps * (32 / lpr));
@@ -747,8 +749,11 @@ int loss_chunks(int L, int n_seq, int E) { MOE_BY_SHAPE(chunks_of_shape, E, 8, 1
 template <int LPR, int NPL, bool FULL>
 cudaError_t run_route_backward(const RouteBackwardArgs& a, cudaStream_t stream) {
   const int L = a.T / a.n_seq;
-  const int chunks = chunks_of(L, a.n_seq, LPR, back_blocks_per_sm(LPR, NPL));
   const bool aux = a.grad_losses != nullptr;
+  // without the losses a row is a few loads and many stores, which three waves
+  // of blocks overlap (weights alone, T = 32768: E = 512 17.6 -> 14.3 us, E = 896
+  // 27.2 -> 22.9; with the losses one wave is better, 29.1 against 30.4)
+  const int chunks = chunks_of(L, a.n_seq, LPR, (aux ? 1 : 3) * back_blocks_per_sm(LPR, NPL));
   const size_t smem =
       4 * ((aux ? a.E : 0) +
            (a.d_weights ? (size_t)kWarps * (32 / LPR) * buf_stride(a.E, LPR) : 0));
