@@ -135,6 +135,32 @@ MOE_DEVICE float sigmoid_row(const float (&v)[NPL], float m, float (&u)[NPL]) {
   return s.x + s.y;
 }
 
+// Mode 1, gradient: x[i] <- u (1 - u) with u = sigmoid(v[i] + row_shift); adds u
+// to s and a[column] u to dot.  1 - u is e^-l u for l > 0, never a difference of
+// nearly equal numbers: where the balance loss alone reaches a column, its whole
+// gradient has this factor (as 1.f - u it is off by up to 0.5 % at l = 12 and is 0
+// past 17; here e^-l is at hand, so it takes no further special function).
+template <int LPR, int NPL, bool FULL>
+MOE_DEVICE void sigmoid_slope_row(const float (&v)[NPL], float m, const float* a, int E, int lig,
+                                  float (&x)[NPL], float& s, float& dot) {
+  const float2 d = pair(row_shift(m));
+  float2 sum = pair(0.f);
+#pragma unroll
+  for (int i = 0; i < NPL; i += 2) {
+    const float2 n = mul2(add2(make_float2(v[i], v[i + 1]), d), pair(-kLog2E));
+    const float2 e = make_float2(ex2(n.x), ex2(n.y));
+    const float2 t = add2(e, pair(1.f));
+    const float2 u = make_float2(rcp(t.x), rcp(t.y));
+    sum = add2(sum, u);
+    if (FULL || lig + LPR * i < E) dot = fmaf(a[lig + LPR * i], u.x, dot);
+    if (FULL || lig + LPR * (i + 1) < E) dot = fmaf(a[lig + LPR * (i + 1)], u.y, dot);
+    const float2 eu = mul2(e, u);
+    x[i] = u.x * (n.x < 0.f ? eu.x : 1.f - u.x);
+    x[i + 1] = u.y * (n.y < 0.f ? eu.y : 1.f - u.y);
+  }
+  s += sum.x + sum.y;
+}
+
 // 1 / s, 0 for an empty row's sum
 MOE_DEVICE float inverse(float s) { return s == 0.f ? 0.f : rcp(s); }
 
@@ -539,7 +565,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
         gk[j] = have ? __ldg(a.d_weights + t * K + k) : 0.f;
       }
     }
-    // mode 0: e^(v - max); mode 1: the sigmoids, shifted as sigmoid_row does
+    // mode 0: e^(v - max); mode 1: u (1 - u) of the shifted sigmoids u
     float x[NPL];
     float m = 0.f, lse = 0.f, inv = 0.f, inv_exp = 0.f, dot = 0.f;
     if constexpr (AUX) {
@@ -554,15 +580,17 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
         inv_exp = inverse(s);
       }
       if constexpr (kSigmoid) {
-        inv = inverse(group_sum<LPR>(sigmoid_row(v, m, x)));
+        float s = 0.f;
+        sigmoid_slope_row<LPR, NPL, FULL>(v, m, smem, E, lig, x, s, dot);
+        inv = inverse(group_sum<LPR>(s));
       } else {
         inv = inv_exp;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+          if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], x[i], dot);
       }
       if constexpr (kEarly)
         if (routing && (unsigned)id[0] < (unsigned)E) lk = __ldg(a.logits + t * a.ld + id[0]);
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (FULL || lig + LPR * i < E) dot = fmaf(smem[lig + LPR * i], x[i], dot);
       dot = group_sum<LPR>(dot) * inv;
     }
     if (routing) {
@@ -610,7 +638,8 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       }
       __syncwarp();
     }
-    // p (a - dot) = x (a inv - dot inv); in mode 0 the z-loss's p zl joins it
+    // mode 0: p (a - dot) = x (a inv - dot inv), and the z-loss's p zl joins it;
+    // mode 1: p (a - dot) (1 - u) likewise
     const float zl = gz != 0.f ? gz * lse : 0.f;
     const float shift = kSigmoid ? -dot * inv : (zl - dot) * inv;
     const float zq = zl * inv_exp;
@@ -622,9 +651,7 @@ route_backward_kernel(RouteBackwardArgs a, int L, int chunks) {
       if constexpr (AUX && !kSigmoid) {
         d = fmaf(x[i], fmaf(smem[c], inv, shift), d);
       } else if constexpr (AUX) {
-        // here 1 - x loses digits where x is near 1, but next to terms that do not
-        // have that small factor; the selected experts' share has it, see above
-        d = fmaf(x[i] * (1.f - x[i]), fmaf(smem[c], inv, shift), d);
+        d = fmaf(x[i], fmaf(smem[c], inv, shift), d);
         if (gz != 0.f) d = fmaf(zq, ex2((v[i] - m) * kLog2E), d);
       }
       if (RPW == 1 || in) out[c] = RPW == 1 || on ? d : 0.f;
