@@ -1,0 +1,60 @@
+"""GPU: the layer on quantised activations reads the codes that it is given --
+all of them, each row's own, on a workspace that has never held them."""
+import pytest
+import torch
+
+from tests import gpu_util as gu
+from tests.test_gpu_block import ops, quantise, w8a8_case  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# H = 4368: past the 4096 columns of the copy's first pass and the 32 scales of
+# its first pass, the last group 16 columns wide; 272 and 128: one pass, ragged and whole
+SHAPES = [(1, 272), (33, 272), (9, 128), (1, 4368), (7, 4368), (300, 4368)]
+
+
+def poisoned(ops, cfg, t):  # noqa: F811
+    """A layer whose workspace holds 0xFF wherever it need not start at zero."""
+    layer = ops.MoELayer(cfg, t)
+    layer.workspace[layer.layout.logits:].fill_(0xFF)
+    return layer
+
+
+@pytest.mark.parametrize("T,H", SHAPES)
+@pytest.mark.parametrize("shared", [False, True])
+def test_layer_q8_on_a_workspace_of_its_own(ops, T, H, shared):  # noqa: F811
+    spec, t = w8a8_case(H=H, T=T, has_shared=shared)
+    cfg = gu.config_for(ops, spec, T)
+    want = ops.MoELayer(cfg, t)(t["x"])
+    xq, xs = quantise(t["x"])
+    layer, got = poisoned(ops, cfg, t), torch.empty_like(want)
+    ops.layer_q8(cfg, t["x"], xq, xs, layer.weights, got, layer.workspace, layer.dev_status)
+    torch.cuda.synchronize()
+    assert int(layer.dev_status) == 0 and want.isfinite().all() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T,H", SHAPES)
+def test_layer_q8_takes_the_experts_rows_from_the_codes(ops, T, H):  # noqa: F811
+    """Codes of another batch: the routing stays x's, the experts' part is the other batch's."""
+    spec, t = w8a8_case(H=H, T=T)
+    K, E, I = spec.K, spec.E, spec.I
+    cfg = gu.config_for(ops, spec, T)
+    g = torch.Generator("cuda").manual_seed(T + H)
+    other = torch.randn(T, H, device="cuda", generator=g).to(torch.bfloat16)
+    layer, got = poisoned(ops, cfg, t), torch.empty_like(other)
+    ops.layer_q8(cfg, t["x"], *quantise(other), layer.weights, got, layer.workspace, layer.dev_status)
+    i32 = torch.int32
+    f2r, offsets = layer.view("flat_to_row", i32, (T * K,)), layer.view("offsets", i32, (E + 1,))
+    weights = layer.view("weights", torch.float32, (T, K))
+    # the same from the operators, quantising the permuted rows themselves
+    xp = torch.empty(T * K, H, dtype=torch.bfloat16, device="cuda")
+    xp[f2r.long()] = other.repeat_interleave(K, 0)
+    hact = torch.empty(T * K, I, dtype=torch.bfloat16, device="cuda")
+    y, want = torch.empty_like(xp), torch.empty_like(other)
+    scratch = torch.zeros(ops.grouped_gemm_scratch_bytes(T * K, E, H, I, ops.W8A8_FP8), dtype=torch.uint8, device="cuda")
+    ops.grouped_gemm(xp, offsets, E, H, I, t["w1"], t["w3"], t["w2"], hact, y, scratch, wdtype=ops.W8A8_FP8,
+                     s1=t["s1"], s3=t["s3"], s2=t["s2"])
+    ops.unpermute(y, f2r, weights, T, K, H, want)
+    ref = ops.MoELayer(cfg, t)(t["x"])
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and not torch.equal(got, ref)
