@@ -340,6 +340,23 @@ def unpermute_backward(dout, flat_to_row, weights, T, K, H, *, y=None, dy=None, 
            "moe_unpermute_backward")
 
 
+def _check_tensors(*specs):
+    """Number of values (None: any), types, contiguity and place of (tensor, types, values, name)
+    each, as the C module checks them; None as a tensor is left to the library."""
+    specs = [s for s in specs if s[0] is not None]
+    for t, _, n, name in specs:
+        if n is not None and t.numel() != n:
+            raise ValueError(f"{name}: {n} values expected, got shape {tuple(t.shape)}")
+    for t, types, _, name in specs:
+        if t.dtype not in types:
+            raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(map(str, types))}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: a contiguous tensor expected, got strides {t.stride()}")
+    for t, _, _, name in specs:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: a tensor on the GPU expected")
+
+
 def layer(cfg: Config, x, weights: Weights, out, workspace, dev_status=None, stream=None, T=None):
     T = x.shape[0] if T is None else T
     _check(_lib().moe_layer(ctypes.byref(cfg), T, _p(x), ctypes.byref(weights), _p(out),
@@ -351,10 +368,12 @@ def layer_q8(cfg: Config, x, xq, xq_scale, weights: Weights, out, workspace, dev
              stream=None):
     """moe_layer on activations that are e4m3 codes already (W8A8 experts; see the header)."""
     T = x.shape[0]
-    for t, n, name in ((x, T * cfg.H, "x"), (xq, T * cfg.H, "xq"),
-                       (xq_scale, T * -(-cfg.H // 128), "xq_scale"), (out, T * cfg.H, "out")):
-        if t.numel() != n:
-            raise ValueError(f"{name}: {n} values expected, got shape {tuple(t.shape)}")
+    bf16, f32 = (torch.bfloat16,), (torch.float32,)
+    _check_tensors((x, bf16, T * cfg.H, "x"),
+                   (xq, (torch.float8_e4m3fn, torch.uint8), T * cfg.H, "xq"),
+                   (xq_scale, f32, T * -(-cfg.H // 128), "xq_scale"), (out, bf16, T * cfg.H, "out"),
+                   (workspace, (torch.uint8,), None, "workspace"),
+                   (dev_status, (torch.int32,), 1, "dev_status"))
     _check(_lib().moe_layer_q8(ctypes.byref(cfg), T, _p(x), _p(xq), _p(xq_scale),
                                ctypes.byref(weights), _p(out), _p(workspace), workspace.numel(),
                                _p(dev_status), _stream(stream)), "moe_layer_q8")
