@@ -430,6 +430,7 @@ class MoEBlock:
 
     def __call__(self, x, residual=None, out=None, stream=None):
         T = x.shape[0]
+        _check_tensors((out, (torch.bfloat16,), T * self.layer.cfg.H, "out"))
         h = torch.empty_like(x) if residual is not None else None
         out = torch.empty_like(x) if out is None else out
         y, L = self.y[:T], self.layer

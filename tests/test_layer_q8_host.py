@@ -55,3 +55,13 @@ def test_layer_q8_refuses_sizes(ops, name, other):
 def test_layer_q8_refuses_tensors_of_the_host(ops):
     with pytest.raises(ValueError, match="^x: a tensor on the GPU"):
         call(ops)
+
+
+@pytest.mark.parametrize("wdtype", ["W_BF16", "W8A8_FP8"])
+@pytest.mark.parametrize("out", [torch.zeros(4, 256), torch.zeros(3, 256, dtype=BF16), torch.zeros(4, 256, dtype=torch.uint8),
+                                 torch.zeros(256, 4, dtype=BF16).t(), torch.zeros(4, 256, dtype=BF16)])
+def test_block_refuses_an_output_that_it_cannot_fill(ops, wdtype, out):
+    cfg = ops.make_config(64, 256, 8, 2, 128, wdtype=getattr(ops, wdtype))
+    block = ops.MoEBlock(cfg, {}, torch.ones(256, dtype=BF16), device="cpu")
+    with pytest.raises(ValueError, match="^out: "):
+        block(torch.zeros(4, 256, dtype=BF16), out=out)
