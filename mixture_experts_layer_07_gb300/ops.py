@@ -156,6 +156,15 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _empty_like(x, stream):
+    """A tensor like x that `stream` fills: of that stream's memory, as torch allocates inside
+    torch.cuda.stream(stream) -- memory freed on another stream may still be in use there."""
+    if stream is None or not x.is_cuda:
+        return torch.empty_like(x)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=x.device)):
+        return torch.empty_like(x)
+
+
 def _check(code, where):
     if code != 0:
         raise MoEError(code, where)
@@ -382,7 +391,9 @@ def layer_q8(cfg: Config, x, xq, xq_scale, weights: Weights, out, workspace, dev
 class MoELayer:
     """Owns the config, the device workspace and the weight pointers of one
     layer and calls ``moe_layer``.  Tensors are kept referenced so their
-    pointers stay valid."""
+    pointers stay valid.  The workspace serves one call at a time: calls on
+    different streams have to be ordered by the caller.  An output that a call
+    allocates belongs to the stream that the call runs on."""
 
     def __init__(self, cfg: Config, tensors: dict, device="cuda"):
         self.cfg = cfg
@@ -398,7 +409,7 @@ class MoELayer:
 
     def __call__(self, x, out=None, stream=None):
         if out is None:
-            out = torch.empty_like(x)
+            out = _empty_like(x, stream)
         layer(self.cfg, x, self.weights, out, self.workspace, self.dev_status, stream)
         return out
 
@@ -416,7 +427,9 @@ class MoEBlock:
     """A pre-norm block: h = x + residual, y = rmsnorm(h) * weight, out = MoELayer(y).
 
     With W8A8 experts the norm also writes y's e4m3 codes and the layer reads those.  Calls with
-    up to cfg.T_max tokens; returns (out, h), of which h is the residual stream's next value."""
+    up to cfg.T_max tokens; returns (out, h), of which h is the residual stream's next value.
+    As with MoELayer, the block's buffers serve one call at a time, and what a call allocates
+    belongs to the stream that it runs on."""
 
     def __init__(self, cfg: Config, tensors: dict, norm_weight, eps=1e-6, device="cuda"):
         self.layer = MoELayer(cfg, tensors, device)
@@ -431,8 +444,8 @@ class MoEBlock:
     def __call__(self, x, residual=None, out=None, stream=None):
         T = x.shape[0]
         _check_tensors((out, (torch.bfloat16,), T * self.layer.cfg.H, "out"))
-        h = torch.empty_like(x) if residual is not None else None
-        out = torch.empty_like(x) if out is None else out
+        h = _empty_like(x, stream) if residual is not None else None
+        out = _empty_like(x, stream) if out is None else out
         y, L = self.y[:T], self.layer
         if self.q8:
             yq, ys = self.yq[:T], self.yq_scale[:T]

@@ -58,3 +58,53 @@ def test_layer_q8_takes_the_experts_rows_from_the_codes(ops, T, H):  # noqa: F81
     ref = ops.MoELayer(cfg, t)(t["x"])
     torch.cuda.synchronize()
     assert torch.equal(got, want) and not torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("what", ["layer", "block"])
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("T", [1, 300])
+def test_outputs_belong_to_the_stream_that_fills_them(ops, what, handle, T):  # noqa: F811
+    """Memory goes back to the stream that it came from, so an output must come from the stream
+    that writes it: neither may it be memory that the current stream has just given up, nor may
+    the current stream get it back while the other one still works on it."""
+    spec, t = w8a8_case(H=272, T=T)
+    cfg = gu.config_for(ops, spec, T)
+    x, r = t["x"], torch.ones_like(t["x"])
+    norm = torch.ones(272, dtype=torch.bfloat16, device="cuda")
+    call = (lambda **k: (ops.MoELayer(cfg, t)(x, **k),)) if what == "layer" else \
+        (lambda **k: ops.MoEBlock(cfg, t, norm)(x, r, **k))
+    want = call()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    gone = [torch.empty_like(x) for _ in range(8)]
+    given_up = {g.data_ptr() for g in gone}
+    del gone
+    got = call(stream=s.cuda_stream if handle else s)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    filled = {g.data_ptr() for g in got}
+    assert not filled & given_up
+    del got, a
+    now = [torch.empty_like(x) for _ in range(64)]
+    assert not filled & {n.data_ptr() for n in now}
+
+
+def test_block_on_another_stream_in_a_graph(ops):  # noqa: F811
+    spec, t = w8a8_case(H=272, T=40)
+    cfg = gu.config_for(ops, spec, 40)
+    norm = torch.ones(272, dtype=torch.bfloat16, device="cuda")
+    block, r = ops.MoEBlock(cfg, t, norm), torch.ones_like(t["x"])
+    want = block(t["x"], r)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = block(t["x"], r, stream=s)
+    for g in got:
+        g.zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
