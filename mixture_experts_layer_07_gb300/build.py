@@ -74,10 +74,13 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr, flush=True)
 
-    # the Python module: host code, compiled along with the kernels
+    # the Python module: host code, compiled along with the kernels.  Without Python's headers
+    # the library is built all the same, for the entry points that do not go through the module.
     src = os.path.join(CSRC, "binding.cpp")
     bind = None
-    if _stale(BINDING, [src] + headers):
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        print(f"no Python.h: {BINDING} is not built", file=sys.stderr, flush=True)
+    elif _stale(BINDING, [src] + headers):
         bind = [cc, "-O2", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-cudart", "none", "-I",
                 INCLUDE, "-I", sysconfig.get_paths()["include"], src, "-o", BINDING + ".tmp"]
         jobs.append(bind)

@@ -10,6 +10,7 @@ computes.  If the library is not built the import of any function raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -73,18 +74,22 @@ class WorkspaceLayout(ctypes.Structure):
 
 
 _L = None
-_B = None  # _moe_binding, once the library is loaded
+_B = None  # _moe_binding, once an operator that goes through it is called
 _P, _I, _F, _S, _I64 = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t,
                         ctypes.c_int64)
 
 
+def _built(path):
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is not built: run __graft_entry__.build() "
+                           "(the MoE path has no fallback)")
+    return path
+
+
 def _lib():
-    global _L, _B
+    global _L
     if _L is None:
-        if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
-            raise RuntimeError(f"{LIB_PATH} is not built: run __graft_entry__.build() "
-                               "(the MoE path has no fallback)")
-        lib = ctypes.CDLL(LIB_PATH)
+        lib = ctypes.CDLL(_built(LIB_PATH))
         lib.moe_status_string.restype = ctypes.c_char_p
         lib.moe_status_string.argtypes = [_I]
         lib.moe_default_m_skinny.restype = _I
@@ -125,16 +130,27 @@ def _lib():
             fn = getattr(lib, name)
             fn.restype = _I
             fn.argtypes = args
-        from . import _moe_binding
-        _moe_binding.connect(*[ctypes.cast(getattr(lib, "moe_" + n), _P).value for n in
-                               ("add_rmsnorm", "add_rmsnorm_backward", "balance_loss",
-                                "route_backward", "unpermute_backward")])
-        _L, _B = lib, _moe_binding
+        _L = lib
     return _L
 
 
 def lib():
     return _lib()
+
+
+def binding():
+    """The C module of the operators around the layer; nothing else needs it."""
+    global _B
+    if _B is None:
+        name = __package__ + "._moe_binding"
+        spec = importlib.util.spec_from_file_location(name, _built(BINDING_PATH))
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.connect(*[ctypes.cast(getattr(_lib(), "moe_" + n), _P).value for n in
+                         ("add_rmsnorm", "add_rmsnorm_backward", "balance_loss",
+                          "route_backward", "unpermute_backward")])
+        _B = module
+    return _B
 
 
 def _p(t):
@@ -288,17 +304,11 @@ def unpermute(y, flat_to_row, weights, T, K, H, out, shared_y=None, shared_gate=
                                 _p(shared_gate), _p(out), _stream(stream)), "moe_unpermute")
 
 
-def _bind():
-    if _B is None:
-        _lib()
-    return _B
-
-
 def add_rmsnorm(x, weight, eps, y, *, residual=None, h=None, rstd=None, yq=None, yq_scale=None,
                 q_group=128, stream=None):
     """y = rmsnorm(x + residual) * weight, h = x + residual; yq / yq_scale: y as e4m3 codes with
     a scale per 128 columns (q_group 128) or per row (q_group 0)."""
-    _check(_bind().add_rmsnorm(x, weight, eps, y, residual, h, rstd, yq, yq_scale, q_group, stream),
+    _check(binding().add_rmsnorm(x, weight, eps, y, residual, h, rstd, yq, yq_scale, q_group, stream),
            "moe_add_rmsnorm")
 
 
@@ -311,7 +321,7 @@ def add_rmsnorm_backward_scratch_bytes(T: int, H: int) -> int:
 
 def add_rmsnorm_backward(dy, h, rstd, weight, dx, dweight, scratch, *, dh=None, stream=None):
     """dx (of x and the residual alike) and dweight [H] fp32; scratch: uint8."""
-    _check(_bind().add_rmsnorm_backward(dy, h, rstd, weight, dx, dweight, scratch, dh, stream),
+    _check(binding().add_rmsnorm_backward(dy, h, rstd, weight, dx, dweight, scratch, dh, stream),
            "moe_add_rmsnorm_backward")
 
 
@@ -326,7 +336,7 @@ def balance_loss(logits, ids, E, counts, mean_prob, valid, losses, scratch, *, n
                  mode=MODE_SOFTMAX, token_mask=None, dev_status=None, stream=None):
     """counts, mean_prob [n_seq, E], valid [n_seq + 2] and losses [2] (load balance, router z) of
     a routed batch; scratch: uint8, zero before its first use; see the header."""
-    _check(_bind().balance_loss(logits, ids, E, counts, mean_prob, valid, losses, scratch, n_seq,
+    _check(binding().balance_loss(logits, ids, E, counts, mean_prob, valid, losses, scratch, n_seq,
                                 mode, token_mask, dev_status, stream), "moe_balance_loss")
 
 
@@ -335,7 +345,7 @@ def route_backward(logits, ids, E, dlogits, *, mode=MODE_SOFTMAX, scale=1.0, wei
                    valid=None, grad_losses=None, dev_status=None, stream=None):
     """dlogits from the gradients of the routing weights, the shared gate and balance_loss's two
     losses; see the header."""
-    _check(_bind().route_backward(logits, ids, E, dlogits, mode, scale, weights, d_weights,
+    _check(binding().route_backward(logits, ids, E, dlogits, mode, scale, weights, d_weights,
                                   d_shared_gate, token_mask, n_seq, counts, valid, grad_losses,
                                   dev_status, stream), "moe_route_backward")
 
@@ -344,7 +354,7 @@ def unpermute_backward(dout, flat_to_row, weights, T, K, H, *, y=None, dy=None, 
                        shared_y=None, shared_gate=None, d_shared_y=None, d_shared_gate=None,
                        stream=None):
     """Gradients of unpermute: dy, d_weights, d_shared_y, d_shared_gate, each where given."""
-    _check(_bind().unpermute_backward(dout, flat_to_row, weights, T, K, H, y, dy, d_weights,
+    _check(binding().unpermute_backward(dout, flat_to_row, weights, T, K, H, y, dy, d_weights,
                                       shared_y, shared_gate, d_shared_y, d_shared_gate, stream),
            "moe_unpermute_backward")
 
