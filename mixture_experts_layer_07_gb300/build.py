@@ -21,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
-BINDING = os.path.join(PKG, "_moe_binding.so")
+# the interpreter's ABI is part of the name: each version has its own file
+BINDING = os.path.join(PKG, "_moe_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

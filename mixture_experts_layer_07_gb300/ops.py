@@ -12,12 +12,13 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import sysconfig
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_gb300.so")
-BINDING_PATH = os.path.join(_HERE, "_moe_binding.so")
+BINDING_PATH = os.path.join(_HERE, "_moe_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 MODE_SOFTMAX, MODE_SIGMOID_BIAS = 0, 1
 W_BF16, W_FP8, W_MXFP4, W8A8_FP8 = 0, 1, 2, 3

@@ -48,3 +48,11 @@ def test_the_operators_still_reach_the_library(ops):
         ops.add_rmsnorm(x, x[0].clone(), 1e-6, torch.zeros_like(x))
     with pytest.raises(ops.MoEError):
         ops.add_rmsnorm_backward_scratch_bytes(4, 20)
+
+
+def test_the_module_of_another_interpreter_is_not_taken_for_this_one(ops):
+    """The file's name carries the ABI that it was compiled for."""
+    import sysconfig
+    assert ops.BINDING_PATH == build_mod.BINDING
+    assert build_mod.BINDING.endswith("_moe_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+    assert os.path.basename(build_mod.BINDING) != "_moe_binding.so"
