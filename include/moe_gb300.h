@@ -369,8 +369,12 @@ moe_status_t moe_unpermute(const void* y, const int32_t* flat_to_row, const floa
  * h may be x or residual themselves, y may be x (when h is not); the outputs
  * otherwise overlap nothing.  H % 16 == 0, H <= 32768 (else
  * MOE_ERR_UNSUPPORTED); pointers of bf16, e4m3 and the weight 16-byte aligned.
- * A row of h holding a NaN or an infinity gives NaN codes and scales.  A row's
- * outputs depend on that row and H alone, bit for bit, not on T.
+ * A row of h holding a NaN gives NaN in all of its y, codes and scales.  One
+ * holding an infinity, and no NaN, has s = 0: y is NaN at the infinity and 0
+ * elsewhere, the scale and the codes of the infinity's group are NaN and those
+ * of the row's other groups 0.  A finite row whose sum of squares passes the
+ * fp32 range (values above about 1.8e19) has s = 0 too: y, codes and scales 0.
+ * A row's outputs depend on that row and H alone, bit for bit, not on T.
  */
 moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* weight,
                              int weight_dtype, int T, int H, float eps, void* h, void* y,

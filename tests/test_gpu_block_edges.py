@@ -54,3 +54,46 @@ def test_sigmoid_gradient_keeps_its_digits(ops, E, K, centre, part):  # noqa: F8
     # constant), the sums by 160 u; row_range holds the largest |l|
     rel = (3 * row_range(l, E, np.ones(T, bool)) + 256) * U
     within(f64(out), ref, rel * mag, "dlogits")
+
+
+# ------------------------------------------------------------------ norm: rows that are not finite
+@pytest.mark.parametrize("H", [16, 256, 2880, 8208])
+@pytest.mark.parametrize("T", [9, 400])
+def test_norm_of_rows_that_are_not_finite_group_by_group(ops, T, H):  # noqa: F811
+    """As the header has it: a NaN takes its whole row, an infinity its own group, and a finite row
+    whose squares overflow comes out as zeros; the rows beside them are as without them."""
+    g = torch.Generator("cuda").manual_seed(H)
+    x, r = (torch.randn(T, H, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    w = (1 + 0.2 * torch.randn(H, device="cuda", generator=g)).to(torch.bfloat16)
+    clean = x.clone(), r.clone()
+    col = {1: H // 2, 2: H - 1, 3: 0, 5: H // 3}
+    x[1, col[1]] = float("nan")
+    r[2, col[2]] = float("inf")
+    x[3, col[3]] = -float("inf")
+    x[4] = 3e19 * (1 + torch.arange(H, device="cuda") % 5)
+    x[5, col[5]], r[5, col[5]] = float("inf"), -float("inf")  # their sum is a NaN
+    odd = [1, 2, 3, 4, 5]
+    even = [t for t in range(T) if t not in odd]
+    for q in (128, 0):
+        def norm(a, b):
+            o = [torch.empty_like(a), torch.empty_like(a), torch.empty(T, device="cuda"),
+                 torch.empty(T, H, dtype=torch.float8_e4m3fn, device="cuda"),
+                 torch.empty(T, -(-H // 128) if q else 1, device="cuda")]
+            ops.add_rmsnorm(a, w, 1e-6, o[0], residual=b, h=o[1], rstd=o[2], yq=o[3], yq_scale=o[4], q_group=q)
+            return o[0].float(), o[1].float(), o[2], o[3].float(), o[4]
+        y, h, rstd, code, scale = norm(x, r)
+        for a, b in zip((y, h, rstd, code, scale), norm(*clean)):
+            assert torch.equal(a[even], b[even])
+        assert torch.equal(h.nan_to_num(1.0, 2.0, 3.0), (x.float() + r.float()).to(torch.bfloat16).float().nan_to_num(1.0, 2.0, 3.0))
+        for t in (1, 5):
+            assert rstd[t].isnan() and y[t].isnan().all() and code[t].isnan().all() and scale[t].isnan().all()
+        for t in (2, 3):
+            assert rstd[t] == 0
+            rest = torch.arange(H, device="cuda") != col[t]
+            assert y[t, col[t]].isnan() and (y[t, rest] == 0).all()
+            group = (torch.arange(H, device="cuda") // (q or H)) == col[t] // (q or H)
+            assert code[t, group].isnan().all() and (code[t, ~group] == 0).all()
+            mine = torch.arange(scale.shape[1], device="cuda") == col[t] // (q or H)
+            assert scale[t, mine].isnan().all() and (scale[t, ~mine] == 0).all()
+        assert rstd[4] == 0 and (y[4] == 0).all() and (code[4] == 0).all() and (scale[4] == 0).all()
+        assert h[4].isfinite().all()
