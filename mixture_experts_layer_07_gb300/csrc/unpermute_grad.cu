@@ -101,6 +101,7 @@ unpermute_backward_kernel(const uint4* __restrict__ dout, const uint4* y,
     }
 #pragma unroll
     for (int i = 0; i < KB; ++i) {
+      if (row[i] < 0) acc[i] = 0.f;  // a dropped replica, whatever dout holds
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
       if (lane_id() == 0) red[slot][i][warp_id()] = acc[i];

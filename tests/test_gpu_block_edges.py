@@ -97,3 +97,26 @@ def test_norm_of_rows_that_are_not_finite_group_by_group(ops, T, H):  # noqa: F8
             assert scale[t, mine].isnan().all() and (scale[t, ~mine] == 0).all()
         assert rstd[4] == 0 and (y[4] == 0).all() and (code[4] == 0).all() and (scale[4] == 0).all()
         assert h[4].isfinite().all()
+
+
+# ------------------------------------------------------------------ combine: dropped replicas
+@pytest.mark.parametrize("T,K,H", [(1, 3, 64), (7, 5, 272), (400, 4, 2880), (3, 2, 32768)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_dropped_replica_has_no_gradient_where_dout_is_not_finite(ops, T, K, H, value):  # noqa: F811
+    g = torch.Generator("cuda").manual_seed(T + K)
+    b = torch.bfloat16
+    dout, y = torch.randn(T, H, device="cuda", generator=g).to(b), torch.randn(T * K, H, device="cuda", generator=g).to(b)
+    w = torch.randn(T, K, device="cuda", generator=g)
+    f2r = torch.randperm(T * K, device="cuda", generator=g).to(torch.int32)
+    dropped = torch.zeros(T, K, dtype=torch.bool, device="cuda")
+    dropped[0, 1] = dropped[T - 1, 0] = True
+    f2r.view(T, K)[0, 1], f2r.view(T, K)[T - 1, 0] = -1, T * K
+    dout[[0, T - 1], H - 1] = value
+    dy, dw = torch.full_like(y, 3.0), torch.full_like(w, 3.0)
+    ops.unpermute_backward(dout, f2r, w, T, K, H, y=y, dy=dy, d_weights=dw)
+    assert (dw[dropped] == 0).all()
+    kept = dw[~dropped]
+    assert (~kept.isfinite()).sum() == (~dropped[[0, T - 1]]).sum() // (2 if T == 1 else 1)
+    bad = ~dy.isfinite().all(1)
+    rows = f2r.view(T, K)[[0, T - 1]][~dropped[[0, T - 1]]].unique().long()
+    assert bad[rows].all() and bad.sum() == len(rows)
