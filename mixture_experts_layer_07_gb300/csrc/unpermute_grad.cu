@@ -54,20 +54,21 @@ unpermute_backward_kernel(const uint4* __restrict__ dout, const uint4* y,
     const int c = threadIdx.x + blockDim.x * j;
     bf16x8_to_f32(c < H8 ? __ldg(dout + (size_t)t * H8 + c) : make_uint4(0u, 0u, 0u, 0u), d[j]);
   }
-  const int n = K + (d_shared_y || d_shared_gate ? 1 : 0);
+  // unsigned: K may be the largest int, and a step of the grid passes it
+  const unsigned n = (unsigned)K + (d_shared_y || d_shared_gate ? 1 : 0);
   int slot = 0;
-  for (int k0 = blockIdx.y * KB; k0 < n; k0 += gridDim.y * KB, slot ^= 1) {
+  for (unsigned k0 = blockIdx.y * KB; k0 < n; k0 += gridDim.y * KB, slot ^= 1) {
     float acc[KB];
     long long row[KB];
     float wk[KB];
     bool shared[KB];
 #pragma unroll
     for (int i = 0; i < KB; ++i) {
-      const int k = k0 + i;
-      shared[i] = k == K && k < n;
+      const unsigned k = k0 + i;
+      shared[i] = k == (unsigned)K && k < n;
       row[i] = -1;
       wk[i] = 0.f;
-      if (k < K && flat_to_row) {
+      if (k < (unsigned)K && flat_to_row) {
         const long long r = __ldg(flat_to_row + (size_t)t * K + k);
         row[i] = r < R ? r : -1;
         if (dy) wk[i] = __ldg(weights + (size_t)t * K + k);
@@ -107,11 +108,11 @@ unpermute_backward_kernel(const uint4* __restrict__ dout, const uint4* y,
       if (lane_id() == 0) red[slot][i][warp_id()] = acc[i];
     }
     __syncthreads();
-    if (threadIdx.x < KB && k0 + (int)threadIdx.x < n) {
-      const int k = k0 + threadIdx.x;
+    if (threadIdx.x < KB && k0 + threadIdx.x < n) {
+      const unsigned k = k0 + threadIdx.x;
       float s = 0.f;
       for (int w = 0; w < nw; ++w) s += red[slot][threadIdx.x][w];
-      if (k < K) {
+      if (k < (unsigned)K) {
         if (d_weights) d_weights[(size_t)t * K + k] = s;
       } else if (d_shared_gate) {
         d_shared_gate[t] = s;
@@ -136,9 +137,11 @@ cudaError_t launch_unpermute_backward(const void* dout, const void* y, const int
            : vpt == 3 ? unpermute_backward_kernel<3, 4>
            : vpt == 4 ? unpermute_backward_kernel<4, 4>
                       : unpermute_backward_kernel<8, 2>;
-  const int groups = moe_cdiv(K + (d_shared_y || d_shared_gate ? 1 : 0), kb);
+  const int groups = moe_cdiv((long long)K + (d_shared_y || d_shared_gate ? 1 : 0), kb);
+  constexpr int kMaxY = 65535;  // of a grid
+  const int split = T >= 2 * 152 ? 1 : groups < kMaxY ? groups : kMaxY;
   // inputs that no requested output needs are not read
-  return moe_launch(k, dim3(T, T < 2 * 152 ? groups : 1), dim3(threads), 0, stream, 1, static_cast<const uint4*>(dout),
+  return moe_launch(k, dim3(T, split), dim3(threads), 0, stream, 1, static_cast<const uint4*>(dout),
                     static_cast<const uint4*>(d_weights ? y : nullptr),
                     dy || d_weights ? flat_to_row : nullptr, weights, T, K, H8,
                     static_cast<const uint4*>(d_shared_gate ? shared_y : nullptr), shared_gate,

@@ -120,3 +120,28 @@ def test_dropped_replica_has_no_gradient_where_dout_is_not_finite(ops, T, K, H, 
     bad = ~dy.isfinite().all(1)
     rows = f2r.view(T, K)[[0, T - 1]][~dropped[[0, T - 1]]].unique().long()
     assert bad[rows].all() and bad.sum() == len(rows)
+
+
+@pytest.mark.parametrize("T,K,H", [(1, 262141, 8), (2, 300001, 16), (1, 131071, 32768)])
+def test_combine_gradient_of_more_replicas_than_a_grid_has_rows(ops, T, K, H):  # noqa: F811
+    """Few tokens spread their replicas over the grid's second axis, which ends at 65535 blocks."""
+    g = torch.Generator("cuda").manual_seed(K)
+    b = torch.bfloat16
+    dout, sy = torch.randn(T, H, device="cuda", generator=g).to(b), torch.randn(T, H, device="cuda", generator=g).to(b)
+    y = torch.randint(-2, 3, (T * K, H), device="cuda", generator=g, dtype=torch.int8).to(b)
+    w, sg = torch.randn(T, K, device="cuda", generator=g), torch.randn(T, device="cuda", generator=g)
+    f2r = torch.randperm(T * K, device="cuda", generator=g).to(torch.int32)
+    dy, dw = torch.full_like(y, 3.0), torch.full_like(w, 3.0)
+    dsy, dsg = torch.empty_like(sy), torch.empty_like(sg)
+    ops.unpermute_backward(dout, f2r, w, T, K, H, y=y, dy=dy, d_weights=dw, shared_y=sy, shared_gate=sg,
+                           d_shared_y=dsy, d_shared_gate=dsg)
+    token, rows = torch.arange(T, device="cuda").repeat_interleave(K), f2r.long()
+    for i in range(0, T * K, 1 << 14):  # a product's one rounding, and bf16's
+        part = slice(i, i + (1 << 14))
+        d = dout[token[part]]
+        assert torch.equal(dy[rows[part]], (w.view(-1, 1)[part] * d.float()).to(b))
+        yd = y[rows[part]].double() * d.double()
+        assert ((dw.view(-1)[part] - yd.sum(1)).abs() <= 96 * U * yd.abs().sum(1)).all()
+    assert torch.equal(dsy, (sg[:, None] * dout.float()).to(b))
+    sd = sy.double() * dout.double()
+    assert ((dsg - sd.sum(1)).abs() <= 96 * U * sd.abs().sum(1)).all()
