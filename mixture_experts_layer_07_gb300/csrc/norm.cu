@@ -267,7 +267,7 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restric
   const int nt = blockDim.x;
   const int rpb = nt / tpr, rs = threadIdx.x / tpr, lt = threadIdx.x % tpr;
   const int wpr = tpr >> 5;
-  const int groups = (T + rpb - 1) / rpb;
+  const int groups = (T - 1) / rpb + 1;  // T > 0; T + rpb may pass the largest int
   pdl_wait();
   pdl_trigger();
   // vector j of array arr (dy, h, dh) in stage st

@@ -145,3 +145,28 @@ def test_combine_gradient_of_more_replicas_than_a_grid_has_rows(ops, T, K, H):  
     assert torch.equal(dsy, (sg[:, None] * dout.float()).to(b))
     sd = sy.double() * dout.double()
     assert ((dsg - sd.sum(1)).abs() <= 96 * U * sd.abs().sum(1)).all()
+
+
+# ------------------------------------------------------------------ the largest counts
+def test_norm_gradient_of_the_most_rows(ops):  # noqa: F811
+    """T = 2^31 - 1: the number of row groups has to be formed without T + rows - 1."""
+    torch.cuda.empty_cache()
+    T, H = 2 ** 31 - 1, 16
+    g = torch.Generator("cuda").manual_seed(0)
+    h = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    dx = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")  # dy, and dx over it
+    rstd = torch.ones(T, device="cuda")
+    rows = [0, 5, 1 << 20, (1 << 30) + 3, T - 17, T - 2, T - 1]
+    sh, sdy = (torch.randn(len(rows), H, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    w = torch.ones(H, device="cuda")
+    h[rows], dx[rows] = sh, sdy
+    dw, dw2, sdx = torch.empty(H, device="cuda"), torch.empty(H, device="cuda"), torch.empty_like(sh)
+    scratch = torch.empty(ops.add_rmsnorm_backward_scratch_bytes(T, H), dtype=torch.uint8, device="cuda")
+    ops.add_rmsnorm_backward(dx, h, rstd, w, dx, dw, scratch)
+    ops.add_rmsnorm_backward(sdy, sh, torch.ones(len(rows), device="cuda"), w, sdx, dw2, scratch)
+    assert torch.equal(dx[rows], sdx)
+    # seven products and their sum, in either order
+    terms = (sdy.double() * sh.double()).abs().sum(0)
+    assert ((dw.double() - dw2.double()).abs() <= 16 * U * terms).all()
+    del h, dx, rstd
+    torch.cuda.empty_cache()
