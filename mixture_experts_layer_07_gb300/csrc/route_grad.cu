@@ -478,7 +478,7 @@ __global__ void balance_empty_kernel(int E, int n_seq, int32_t* __restrict__ cou
       counts[i] = 0;
       mean_prob[i] = 0.f;
     }
-    if (i < n_seq + 2) valid[i] = 0;
+    if (i < n_seq + 2ll) valid[i] = 0;
     if (i < 2) losses[i] = 0.f;
   }
 }

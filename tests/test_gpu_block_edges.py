@@ -170,3 +170,19 @@ def test_norm_gradient_of_the_most_rows(ops):  # noqa: F811
     assert ((dw.double() - dw2.double()).abs() <= 16 * U * terms).all()
     del h, dx, rstd
     torch.cuda.empty_cache()
+
+
+def test_losses_of_the_most_empty_sequences(ops):  # noqa: F811
+    """n_seq = 2^31 - 1 without a token: valid has n_seq + 2 entries, past the largest int."""
+    torch.cuda.empty_cache()
+    S = 2 ** 31 - 1
+    c, p = torch.full((S,), -9, dtype=torch.int32, device="cuda"), torch.full((S,), -9.0, device="cuda")
+    v, lo = torch.full((S + 2,), -9, dtype=torch.int32, device="cuda"), torch.full((2,), -9.0, device="cuda")
+    scratch = torch.empty(ops.balance_loss_scratch_bytes(0, 1, S), dtype=torch.uint8, device="cuda")  # not read at T = 0
+    ops.balance_loss(torch.empty(0, 1, device="cuda"), torch.empty(0, 1, dtype=torch.int32, device="cuda"), 1, c, p, v,
+                     lo, scratch, n_seq=S)
+    for t in (c, p, v, lo):
+        for part in t.split(1 << 28):
+            assert not part.any()
+    del c, p, v, scratch, t, part
+    torch.cuda.empty_cache()
