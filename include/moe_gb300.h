@@ -419,8 +419,9 @@ moe_status_t moe_balance_loss_scratch_bytes(int T, int E, int n_seq, size_t* byt
  *   valid           = n[0], ..., n[n_seq - 1], N, S+
  * Both losses are 0 where nothing is kept.  A kept row whose E logits are all
  * -inf counts as a token with p = 0 and log-sum-exp 0; a NaN in a kept row
- * reaches the losses and its sequence's mean_prob; rows that the mask leaves
- * out may hold anything.
+ * reaches the losses and its sequence's mean_prob, as +inf does in mode 0 (in
+ * mode 1 +inf is a sigmoid of 1, and only losses[1] becomes NaN); rows that the
+ * mask leaves out may hold anything.
  *   logits     [T, ld_logits] fp32, ld_logits >= E (columns from E on, such as
  *              the shared gate's, are not read)
  *   ids        [T, K] int32; an id outside [0, E) is not counted and sets
@@ -431,8 +432,9 @@ moe_status_t moe_balance_loss_scratch_bytes(int T, int E, int n_seq, size_t* byt
  *   scratch    >= moe_balance_loss_scratch_bytes(T, E, n_seq), 256-byte
  *              aligned, zero before the first call; every call leaves it zero
  *              again, so calls of other sizes may share it (in stream order)
- * T % n_seq == 0.  T == 0 writes zeros.  Deterministic: sums over blocks are
- * integers.
+ * T % n_seq == 0.  T == 0 writes zeros.  Deterministic: a block's sum of
+ * probabilities is fp32, blocks are added in fixed point with steps of
+ * 2^-(61 - ceil(log2(T / n_seq))), below half of which a block's sum counts as 0.
  */
 moe_status_t moe_balance_loss(const float* logits, int ld_logits, const int32_t* ids,
                               const uint8_t* token_mask, int T, int E, int K, int n_seq, int mode,

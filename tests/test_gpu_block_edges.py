@@ -186,3 +186,29 @@ def test_losses_of_the_most_empty_sequences(ops):  # noqa: F811
             assert not part.any()
     del c, p, v, scratch, t, part
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ router: an infinite logit
+@pytest.mark.parametrize("E", [5, 40, 600])
+def test_router_row_with_an_infinite_logit(ops, E):  # noqa: F811
+    """+inf is a NaN to the softmax and a sigmoid of 1; the other sequence does not see it."""
+    S, L, K = 2, 16, 3
+    g = np.random.default_rng(E)
+    l = g.normal(size=(S * L, E)).astype(np.float32)
+    ids = np.argsort(-l, axis=1)[:, :K].astype(np.int32)
+    big, inf = l.copy(), l.copy()
+    big[5, 2], inf[5, 2] = 200.0, np.inf
+    for mode in (0, 1):
+        c0, p0, v0, lo0 = balance(ops, f32(big), i32(ids), None, E, S, mode)
+        c1, p1, v1, lo1 = balance(ops, f32(inf), i32(ids), None, E, S, mode)
+        assert torch.equal(c0, c1) and torch.equal(v0, v1) and torch.equal(p0[1], p1[1]) and lo1[1].isnan()
+        if mode == 0:
+            assert p1[0].isnan().all() and lo1[0].isnan()
+        else:
+            assert torch.equal(p0, p1) and lo0[0] == lo1[0]
+        out = [torch.empty(S * L, E, device="cuda") for _ in range(2)]
+        for o, a in zip(out, (big, inf)):
+            ops.route_backward(f32(a), i32(ids), E, o, mode=mode, n_seq=S, counts=c0, valid=v0, grad_losses=f32([1.0, 0.0]))
+        rest = [t for t in range(S * L) if t != 5]
+        assert torch.equal(out[0][rest], out[1][rest])
+        assert torch.equal(out[0][5], out[1][5]) if mode else out[1][5].isnan().all()
