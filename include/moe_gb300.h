@@ -375,6 +375,7 @@ moe_status_t moe_unpermute(const void* y, const int32_t* flat_to_row, const floa
  * of the row's other groups 0.  A finite row whose sum of squares passes the
  * fp32 range (values above about 1.8e19) has s = 0 too: y, codes and scales 0.
  * A row's outputs depend on that row and H alone, bit for bit, not on T.
+ * T == 0 does nothing, whatever the pointers are.
  */
 moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* weight,
                              int weight_dtype, int T, int H, float eps, void* h, void* y,
@@ -484,7 +485,8 @@ moe_status_t moe_route_backward(const float* logits, int ld_logits, const int32_
  *   dout [T, H] bf16;  y, dy [T*K, H] bf16;  shared_y, d_shared_y [T, H] bf16;
  *   weights, d_weights [T, K] fp32;  shared_gate, d_shared_gate [T] fp32
  * dy may be y, d_shared_y may be shared_y.  H % 8 == 0, H <= 32768 (else
- * MOE_ERR_UNSUPPORTED).  Deterministic.
+ * MOE_ERR_UNSUPPORTED).  Deterministic.  T == 0 does nothing, whatever the
+ * pointers are.
  */
 moe_status_t moe_unpermute_backward(const void* dout, const void* y, const int32_t* flat_to_row,
                                     const float* weights, int T, int K, int H,

@@ -310,10 +310,10 @@ moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* we
   const moe_status_t s = check_norm(T, H, weight_dtype);
   if (s != MOE_OK) return s;
   if (!(eps > 0.f) || !(eps < 3.4e38f)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;  // an empty tensor's pointer may be NULL
   if ((h && !residual) || (!y && !yq) || (yq == nullptr) != (yq_scale == nullptr))
     return MOE_ERR_INVALID_ARG;
   if (yq && q_group != 0 && q_group != 128) return MOE_ERR_UNSUPPORTED;
-  if (T == 0) return MOE_OK;
   if (!x || !weight) return MOE_ERR_INVALID_ARG;
   if (y && (y == h || y == residual)) return MOE_ERR_INVALID_ARG;
   if (misaligned(x, 16) || misaligned(residual, 16) || misaligned(weight, 16) ||
@@ -415,11 +415,11 @@ moe_status_t moe_unpermute_backward(const void* dout, const void* y, const int32
   if (T < 0 || K <= 0 || H <= 0 || H % 8 != 0) return MOE_ERR_INVALID_ARG;
   if ((int64_t)T * K > 0x7fffffff) return MOE_ERR_INVALID_ARG;
   if (H > kRowMaxH) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;  // an empty tensor's pointer may be NULL
   if (!dy && !d_weights && !d_shared_y && !d_shared_gate) return MOE_ERR_INVALID_ARG;
   if ((d_weights && !y) || (dy && !weights) || (d_shared_gate && !shared_y) ||
       (d_shared_y && !shared_gate))
     return MOE_ERR_INVALID_ARG;
-  if (T == 0) return MOE_OK;
   if (!dout || ((dy || d_weights) && !flat_to_row)) return MOE_ERR_INVALID_ARG;
   if (misaligned(dout, 16) || misaligned(y, 16) || misaligned(dy, 16) ||
       misaligned(shared_y, 16) || misaligned(d_shared_y, 16) || misaligned(flat_to_row, 4) ||
