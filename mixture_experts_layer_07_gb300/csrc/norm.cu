@@ -15,10 +15,10 @@
 // threads (a multiple of the warp), each owning the 16-byte vectors
 // tid + tpr*j, j < VPT; a 128-column scale group is then the 16 vectors of half
 // a warp, so its maximum needs four shuffles.
-// Measured on one GB300 (copy rate 6778 GB/s): T = 8191, H = 7168 with residual
-// and a scale per row 79.8 us, 98 % of the copy rate; T = 4096, H = 2880 with a
-// scale per 128 columns 20.9 us (75 %, 1.7 us of it the launch); T = 1, H = 2048
-// 1.7 us.  Backward T = 8192, H = 7168 75.8 us (91 %).
+// Measured on one GB300 (copy rate 6696 GB/s): T = 8191, H = 7168 with residual
+// and a scale per row 79.7 us, 99 % of the copy rate; T = 4096, H = 2880 with a
+// scale per 128 columns 20.8 us (77 %, 1.7 us of it the launch); T = 1, H = 2048
+// 1.7 us.  Backward T = 8192, H = 7168 75.6 us (93 %).
 #include <cuda_fp8.h>
 
 #include "common.cuh"

@@ -22,11 +22,13 @@
 // Memory bounds both where the batch is large: each row of logits is read once
 // into registers (a group of LPR lanes per row, NPL columns per lane, the next
 // row on its way) and used for every sum.  Measured on one GB300: losses T = 8 x
-// 4096, E = 512, half padded 13.6 us; losses and gradient T = 4 x 2048, E = 896,
-// sigmoid, padded 23.4 us; T = 65536, E = 512 losses 29 us (70 % of the copy
-// rate; 8 us of it are the launch and the hand-over between blocks, the marginal
-// rate is 95 %), gradient 54 us (75 %).  Small batches are bound by latency:
-// T = 2048, E = 128 losses 4.3 us.
+// 4096, E = 512, 41 % kept 13.5 us; losses and gradient T = 4 x 2048, E = 896,
+// sigmoid, 39 % kept 23.4 us; T = 65536, E = 512 losses 29 us (71 % of the copy
+// rate; 8.5 us of it are the launch, the first rows and the hand-over between
+// blocks, the marginal rate is the copy's), gradient 54 us (76 %), of the routing
+// weights alone 26 us (83 %).  Small batches are bound by latency, T = 2048,
+// E = 128 losses 4.35 us; few experts by a token's fixed work, T = 2^20, E = 8
+// losses 26 us (24 %), gradient 53 us (26 %).
 // Determinism: a block's probability sums are fp32 in a fixed order; across
 // blocks they are added as 64-bit fixed point, so the order does not matter.  A
 // step is 2^-(61 - ceil(log2 L)), 2^-49 at L = 4096: half of one per block is the

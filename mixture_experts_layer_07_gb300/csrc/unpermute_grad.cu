@@ -9,7 +9,7 @@
 // spread their groups over gridDim.y blocks.  Bound by memory.  No atomics:
 // every row belongs to one (t, k).
 // Measured on one GB300: T = 8192, K = 10, H = 2048 with the shared expert 116 us,
-// 98 % of the copy rate (164 us with each row's loads behind the last row's
+// 99 % of the copy rate (164 us with each row's loads behind the last row's
 // stores); T = 509, K = 4, H = 2880 5.6 us; T = 1, K = 8, H = 2048 3.0 us (4.7 as
 // one block).
 #include "common.cuh"
