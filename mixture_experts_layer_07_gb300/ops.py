@@ -178,7 +178,10 @@ def _empty_like(x, stream):
     torch.cuda.stream(stream) -- memory freed on another stream may still be in use there."""
     if stream is None or not x.is_cuda:
         return torch.empty_like(x)
-    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=x.device)):
+    handle = _stream(stream)  # 0, the default stream's, would make ExternalStream a new stream
+    s = torch.cuda.ExternalStream(handle, device=x.device) if handle else \
+        torch.cuda.default_stream(x.device)
+    with torch.cuda.stream(s):
         return torch.empty_like(x)
 
 

@@ -108,3 +108,23 @@ def test_block_on_another_stream_in_a_graph(ops):  # noqa: F811
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("inside", [False, True])
+@pytest.mark.parametrize("given", ["default", "zero", "current", "side"])
+def test_outputs_on_the_default_stream_are_its_memory(ops, inside, given):  # noqa: F811
+    """The default stream's handle is 0; the allocator says whose memory an output is."""
+    spec, t = w8a8_case(H=272, T=300)
+    block = ops.MoEBlock(gu.config_for(ops, spec, 300), t, torch.ones(272, dtype=torch.bfloat16, device="cuda"))
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side if inside else torch.cuda.default_stream()):
+        stream = {"default": torch.cuda.default_stream(), "zero": 0, "current": torch.cuda.current_stream(),
+                  "side": other}[given]
+        handle = stream if given == "zero" else stream.cuda_stream
+        got = block(t["x"], torch.ones_like(t["x"]), stream=stream)
+    torch.cuda.synchronize()
+    for g in got:
+        owner, = [s["stream"] for s in torch.cuda.memory_snapshot()
+                  if s["address"] <= g.data_ptr() < s["address"] + s["total_size"]]
+        assert owner == handle
