@@ -403,6 +403,93 @@ moe_status_t moe_add_rmsnorm_backward(const void* dy, const void* dh, const void
                                       int T, int H, void* dx, float* dweight, void* scratch,
                                       size_t scratch_bytes, moe_stream_t stream);
 
+/*
+ * Activations kept in 8 bits for the backward pass: rows as e4m3 codes with an
+ * fp32 scale per 128 columns, the W8A8 activation format (what moe_add_rmsnorm
+ * writes as yq with q_group 128, and what moe_layer_q8 reads).
+ *   pack:    scale = max |x| / 448 of the group (IEEE fp32 division, 0 for an
+ *            all-zero group), code = e4m3(x / scale) rounded to nearest even,
+ *            saturated at 448
+ *   unpack:  x = code * scale, the fp32 product rounded to bf16
+ *   x     [T, H] bf16;  xq [T, H] e4m3;  xq_scale [T, ceil(H / 128)] fp32 (the
+ *         last group of a row may be narrower)
+ * A group that holds an infinity or a NaN does not survive: its scale is not
+ * finite and unpack gives NaN for all of it (for an infinity, NaN or infinities);
+ * other groups are not touched by it.  H % 16 == 0; x and xq 16-byte aligned;
+ * outputs overlap no input.  T == 0 does nothing, whatever the pointers are.
+ */
+moe_status_t moe_pack_q8(const void* x, int T, int H, void* xq, float* xq_scale,
+                         moe_stream_t stream);
+moe_status_t moe_unpack_q8(const void* xq, const float* xq_scale, int T, int H, void* x,
+                           moe_stream_t stream);
+
+/*
+ * moe_add_rmsnorm_backward with h as moe_pack_q8 gives it: n[t] = code * scale *
+ * rstd[t], with rstd as the forward pass stored it (of the unrounded h).  The
+ * codes are decoded to fp32, without a rounding to bf16 between.
+ *   hq [T, H] e4m3, 16-byte aligned;  hq_scale [T, ceil(H / 128)] fp32
+ * Everything else, the scratch among it, as moe_add_rmsnorm_backward.
+ */
+moe_status_t moe_add_rmsnorm_backward_q8(const void* dy, const void* dh, const void* hq,
+                                         const float* hq_scale, const float* rstd,
+                                         const void* weight, int weight_dtype, int T, int H,
+                                         void* dx, float* dweight, void* scratch,
+                                         size_t scratch_bytes, moe_stream_t stream);
+
+/* Scratch bytes moe_experts_backward needs. */
+moe_status_t moe_experts_backward_scratch_bytes(int T, int H, int E, int K, int I, size_t* bytes);
+
+/*
+ * Gradient of permute, grouped GEMM and unpermute as one: from the tokens x, the
+ * routing and the gradient dout of the combined output.  For the replica r of
+ * token t and slot k, on expert e, with g = x[t] . W1[e]^T, u = x[t] . W3[e]^T,
+ * s = sigmoid(g), act = g s u and a = dout[t] . W2[e] (rows of I values):
+ *   d_weights[t, k] = <a, act>                    (0 for a dropped replica)
+ *   dg = weights[t, k] a u s (1 + g (1 - s)),  du = weights[t, k] a g s
+ *   dx[t]  = sum_k (dg . W1[e] + du . W3[e]) + dx_add[t]
+ *   dw1[e] = sum_r dg^T x,  dw3[e] = sum_r du^T x
+ *   dw2[e] = sum_r dout^T (weights act)
+ * g and u are computed again; nothing of the forward pass is read but the
+ * tokens and the routing.  The products run on the tensor cores in bf16 with
+ * fp32 sums: dg, du and (weights act) are rounded to bf16 once, each output
+ * once more; d_weights comes from unrounded values, and dx's rows are fp32
+ * until the K of them are added.
+ *   x         [T, H] bf16, or NULL with
+ *   xq        [T, H] e4m3 and xq_scale [T, ceil(H / 128)] fp32, as moe_pack_q8
+ *             or moe_add_rmsnorm give them: x is then what moe_unpack_q8 gives
+ *   dout      [T, H] bf16
+ *   offsets   [E + 1], row_to_flat [T*K], flat_to_row [T*K] int32 as moe_permute
+ *             (or a layer's workspace) has them; a flat_to_row outside
+ *             [0, offsets[E]) is a dropped replica
+ *   weights   [T, K] fp32
+ *   w1, w3    [E, I, H];  w2 [E, H, I] bf16
+ *   dx_add    [T, H] bf16 or NULL (a gradient that reaches the tokens another
+ *             way, such as through the router)
+ *   dx        [T, H] bf16 output or NULL; may be dx_add, dout or x
+ *   d_weights [T, K] fp32 output or NULL
+ *   dw1, dw3, dw2  outputs of the matrices' shapes, all three or none; of
+ *             dw_dtype MOE_DT_BF16 or MOE_DT_F32.  Experts without a row get
+ *             zeros.  accumulate 1: the gradients are added to what the buffers
+ *             hold (MOE_DT_F32, else MOE_ERR_UNSUPPORTED), and experts without a
+ *             row are not touched
+ *   scratch   >= moe_experts_backward_scratch_bytes(T, H, E, K, I), 256-byte
+ *             aligned, any contents; one call at a time
+ *   dev_status  MOE_DEV_WAIT_TIMEOUT where a pipeline wait gave up, or NULL
+ * Not all of dx, d_weights and dw1 may be NULL.  With E = 1 and K = 1 (offsets
+ * 0, T and both maps 0 .. T-1) it is the gradient of a shared expert, weights
+ * its gate.  Outputs overlap nothing else.  Deterministic.  T == 0 writes zeros
+ * to the matrices' gradients (nothing with accumulate).
+ */
+moe_status_t moe_experts_backward(const void* x, const void* xq, const float* xq_scale,
+                                  const void* dout, const int32_t* offsets,
+                                  const int32_t* row_to_flat, const int32_t* flat_to_row,
+                                  const float* weights, int T, int H, int E, int K, int I,
+                                  const void* w1, const void* w3, const void* w2,
+                                  const void* dx_add, void* dx, float* d_weights, void* dw1,
+                                  void* dw3, void* dw2, int dw_dtype, int accumulate,
+                                  void* scratch, size_t scratch_bytes, int32_t* dev_status,
+                                  moe_stream_t stream);
+
 /* Scratch bytes moe_balance_loss needs. */
 moe_status_t moe_balance_loss_scratch_bytes(int T, int E, int n_seq, size_t* bytes);
 

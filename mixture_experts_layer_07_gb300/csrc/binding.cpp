@@ -24,6 +24,10 @@ decltype(&moe_add_rmsnorm_backward) p_add_rmsnorm_backward;
 decltype(&moe_balance_loss) p_balance_loss;
 decltype(&moe_route_backward) p_route_backward;
 decltype(&moe_unpermute_backward) p_unpermute_backward;
+decltype(&moe_pack_q8) p_pack_q8;
+decltype(&moe_unpack_q8) p_unpack_q8;
+decltype(&moe_add_rmsnorm_backward_q8) p_add_rmsnorm_backward_q8;
+decltype(&moe_experts_backward) p_experts_backward;
 
 enum Kind { BF16, F32, I32, E4M3, MASK, BYTES };
 
@@ -164,9 +168,25 @@ struct Call {
     return static_cast<moe_stream_t>(p);
   }
 
-  // a norm's weight and its element type
-  const void* weight(int i, int H, int* dtype) {
-    if (bad) return nullptr;
+  // the three sizes of a stack of matrices
+  void shape3(int i, const char* name, int* n, int* rows, int* cols) {
+    *n = *rows = *cols = 0;
+    if (bad) return;
+    PyObject* s = PyObject_GetAttr(a[i], s_shape);
+    if (!s || !PyTuple_Check(s) || PyTuple_GET_SIZE(s) != 3) {
+      if (s) PyErr_Format(PyExc_ValueError, "%s: a stack of matrices expected, got shape %S", name, s);
+      bad = true;
+    } else {
+      *n = in_range(PyLong_AsLongLong(PyTuple_GET_ITEM(s, 0)));
+      *rows = in_range(PyLong_AsLongLong(PyTuple_GET_ITEM(s, 1)));
+      *cols = in_range(PyLong_AsLongLong(PyTuple_GET_ITEM(s, 2)));
+    }
+    Py_XDECREF(s);
+  }
+
+  // a tensor of n values, bf16 or fp32, and its element type
+  void* either(int i, long long n, int* dtype, const char* name) {
+    if (bad || a[i] == Py_None) return nullptr;
     PyObject* d = PyObject_GetAttr(a[i], s_dtype);
     if (!d) {
       bad = true;
@@ -175,7 +195,16 @@ struct Call {
     const bool f32 = d == t_f32;
     Py_DECREF(d);
     *dtype = f32 ? MOE_DT_F32 : MOE_DT_BF16;
-    return ptr(i, f32 ? F32 : BF16, H, "weight");
+    return ptr(i, f32 ? F32 : BF16, n, name);
+  }
+  // a norm's weight
+  const void* weight(int i, int H, int* dtype) {
+    if (bad) return nullptr;
+    if (a[i] == Py_None) {  // the library's to refuse
+      *dtype = MOE_DT_BF16;
+      return nullptr;
+    }
+    return either(i, H, dtype, "weight");
   }
 
   void* scratch(int i, size_t* bytes) {
@@ -330,11 +359,102 @@ PyObject* unpermute_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// the five entry points' addresses, in the order of the functions above
+// x, xq, xq_scale, stream
+PyObject* pack_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 4)) return nullptr;
+  Call c{a};
+  int T, H;
+  c.shape2(0, "x", &T, &H);
+  const long long m = (long long)T * H;
+  const void* x = c.ptr(0, BF16, m, "x");
+  void* xq = c.ptr(1, E4M3, m, "xq");
+  float* s = c.ptr<float>(2, F32, (long long)T * ((H + 127) / 128), "xq_scale");
+  const moe_stream_t st = c.stream(3);
+  return run(c, [&] { return p_pack_q8(x, T, H, xq, s, st); });
+}
+
+// xq, xq_scale, x, stream
+PyObject* unpack_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 4)) return nullptr;
+  Call c{a};
+  int T, H;
+  c.shape2(0, "xq", &T, &H);
+  const long long m = (long long)T * H;
+  const void* xq = c.ptr(0, E4M3, m, "xq");
+  const float* s = c.ptr<float>(1, F32, (long long)T * ((H + 127) / 128), "xq_scale");
+  void* x = c.ptr(2, BF16, m, "x");
+  const moe_stream_t st = c.stream(3);
+  return run(c, [&] { return p_unpack_q8(xq, s, T, H, x, st); });
+}
+
+// dy, hq, hq_scale, rstd, weight, dx, dweight, scratch, dh, stream
+PyObject* add_rmsnorm_backward_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 10)) return nullptr;
+  Call c{a};
+  int T, H, wdt = 0;
+  c.shape2(1, "hq", &T, &H);
+  const long long m = (long long)T * H;
+  const void* dy = c.ptr(0, BF16, m, "dy");
+  const void* hq = c.ptr(1, E4M3, m, "hq");
+  const float* hs = c.ptr<float>(2, F32, (long long)T * ((H + 127) / 128), "hq_scale");
+  const float* rstd = c.ptr<float>(3, F32, T, "rstd");
+  const void* w = c.weight(4, H, &wdt);
+  void* dx = c.ptr(5, BF16, m, "dx");
+  float* dw = c.ptr<float>(6, F32, H, "dweight");
+  size_t bytes = 0;
+  void* scratch = c.scratch(7, &bytes);
+  const void* dh = c.ptr(8, BF16, m, "dh");
+  const moe_stream_t st = c.stream(9);
+  return run(c, [&] {
+    return p_add_rmsnorm_backward_q8(dy, dh, hq, hs, rstd, w, wdt, T, H, dx, dw, scratch, bytes, st);
+  });
+}
+
+// dout, offsets, row_to_flat, flat_to_row, weights, w1, w3, w2, scratch, x, xq, xq_scale, dx_add,
+// dx, d_weights, dw1, dw3, dw2, accumulate, dev_status, stream
+PyObject* experts_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 21)) return nullptr;
+  Call c{a};
+  int T, H, Tw, K, E, I, Hw, dt = MOE_DT_BF16;
+  c.shape2(0, "dout", &T, &H);
+  c.shape2(4, "weights", &Tw, &K);
+  c.shape3(5, "w1", &E, &I, &Hw);
+  const long long m = (long long)T * H, r = (long long)T * K, ew = (long long)E * I * H;
+  const void* dout = c.ptr(0, BF16, m, "dout");
+  const int32_t* off = c.ptr<int32_t>(1, I32, (long long)E + 1, "offsets");
+  const int32_t* r2f = c.ptr<int32_t>(2, I32, r, "row_to_flat");
+  const int32_t* f2r = c.ptr<int32_t>(3, I32, r, "flat_to_row");
+  const float* w = c.ptr<float>(4, F32, r, "weights");
+  const void* w1 = c.ptr(5, BF16, ew, "w1");
+  const void* w3 = c.ptr(6, BF16, ew, "w3");
+  const void* w2 = c.ptr(7, BF16, ew, "w2");
+  size_t bytes = 0;
+  void* scratch = c.scratch(8, &bytes);
+  const void* x = c.ptr(9, BF16, m, "x");
+  const void* xq = c.ptr(10, E4M3, m, "xq");
+  const float* xs = c.ptr<float>(11, F32, (long long)T * ((H + 127) / 128), "xq_scale");
+  const void* add = c.ptr(12, BF16, m, "dx_add");
+  void* dx = c.ptr(13, BF16, m, "dx");
+  float* dw = c.ptr<float>(14, F32, r, "d_weights");
+  void* dw1 = c.either(15, ew, &dt, "dw1");
+  const Kind k = dt == MOE_DT_F32 ? F32 : BF16;  // the three have one type
+  void* dw3 = c.ptr(16, k, ew, "dw3");
+  void* dw2 = c.ptr(17, k, ew, "dw2");
+  const int acc = c.integer(18);
+  int32_t* status = c.ptr<int32_t>(19, I32, 1, "dev_status");
+  const moe_stream_t st = c.stream(20);
+  return run(c, [&] {
+    return p_experts_backward(x, xq, xs, dout, off, r2f, f2r, w, T, H, E, K, I, w1, w3, w2, add, dx,
+                              dw, dw1, dw3, dw2, dt, acc, scratch, bytes, status, st);
+  });
+}
+
+// the entry points' addresses, in the order of the functions above
 PyObject* connect(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count(n, 5)) return nullptr;
-  void* p[5];
-  for (int i = 0; i < 5; ++i) {
+  constexpr int kPoints = 9;
+  if (!count(n, kPoints)) return nullptr;
+  void* p[kPoints];
+  for (int i = 0; i < kPoints; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null entry point");
@@ -346,6 +466,10 @@ PyObject* connect(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p_balance_loss = reinterpret_cast<decltype(p_balance_loss)>(p[2]);
   p_route_backward = reinterpret_cast<decltype(p_route_backward)>(p[3]);
   p_unpermute_backward = reinterpret_cast<decltype(p_unpermute_backward)>(p[4]);
+  p_pack_q8 = reinterpret_cast<decltype(p_pack_q8)>(p[5]);
+  p_unpack_q8 = reinterpret_cast<decltype(p_unpack_q8)>(p[6]);
+  p_add_rmsnorm_backward_q8 = reinterpret_cast<decltype(p_add_rmsnorm_backward_q8)>(p[7]);
+  p_experts_backward = reinterpret_cast<decltype(p_experts_backward)>(p[8]);
   Py_RETURN_NONE;
 }
 
@@ -362,6 +486,10 @@ PyMethodDef methods[] = {
     {"balance_loss", as_method(balance_loss), METH_FASTCALL, nullptr},
     {"route_backward", as_method(route_backward), METH_FASTCALL, nullptr},
     {"unpermute_backward", as_method(unpermute_backward), METH_FASTCALL, nullptr},
+    {"pack_q8", as_method(pack_q8), METH_FASTCALL, nullptr},
+    {"unpack_q8", as_method(unpack_q8), METH_FASTCALL, nullptr},
+    {"add_rmsnorm_backward_q8", as_method(add_rmsnorm_backward_q8), METH_FASTCALL, nullptr},
+    {"experts_backward", as_method(experts_backward), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_binding", nullptr, -1, methods,

@@ -62,6 +62,32 @@ moe_status_t check_router(int T, int E, int K, int n_seq, int mode) {
   return MOE_OK;
 }
 
+moe_status_t check_experts(int T, int H, int E, int K, int I) {
+  const moe_status_t s = check_dims(T, H, E, K);
+  if (s != MOE_OK) return s;
+  if (I <= 0 || I % 16 != 0 || (int64_t)T * K > 0x7fffffff / 2) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// the norm's gradient, h as bf16 (hscale NULL) or as codes
+moe_status_t norm_backward(const void* dy, const void* dh, const void* h, const float* hscale,
+                           const float* rstd, const void* weight, int weight_dtype, int T, int H,
+                           void* dx, float* dweight, void* scratch, size_t scratch_bytes,
+                           moe_stream_t stream) {
+  const moe_status_t s = check_norm(T, H, weight_dtype);
+  if (s != MOE_OK) return s;
+  if (!dweight || !scratch) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!dy || !h || !rstd || !weight || !dx)) return MOE_ERR_INVALID_ARG;
+  if (scratch_bytes < add_rmsnorm_backward_scratch_bytes(T, H)) return MOE_ERR_WORKSPACE;
+  if (misaligned(dy, 16) || misaligned(dh, 16) || misaligned(h, 16) || misaligned(weight, 16) ||
+      misaligned(dx, 16) || misaligned(rstd, 4) || misaligned(dweight, 4) ||
+      misaligned(scratch, 256))
+    return MOE_ERR_MISALIGNED;
+  return cuda_status(launch_add_rmsnorm_backward(dy, dh, h, hscale, rstd, weight,
+                                                 weight_dtype == MOE_DT_F32, T, H, dx, dweight,
+                                                 scratch, stream));
+}
+
 // byte offset of the one-launch small-batch layer's counters inside `sync`
 // (after the fused routing's 256 bytes and the K-slice counters)
 size_t decode_sync_offset(const moe_config_t* c) {
@@ -336,18 +362,86 @@ moe_status_t moe_add_rmsnorm_backward(const void* dy, const void* dh, const void
                                       const float* rstd, const void* weight, int weight_dtype,
                                       int T, int H, void* dx, float* dweight, void* scratch,
                                       size_t scratch_bytes, moe_stream_t stream) {
-  const moe_status_t s = check_norm(T, H, weight_dtype);
+  return norm_backward(dy, dh, h, nullptr, rstd, weight, weight_dtype, T, H, dx, dweight, scratch,
+                       scratch_bytes, stream);
+}
+
+moe_status_t moe_add_rmsnorm_backward_q8(const void* dy, const void* dh, const void* hq,
+                                         const float* hq_scale, const float* rstd,
+                                         const void* weight, int weight_dtype, int T, int H,
+                                         void* dx, float* dweight, void* scratch,
+                                         size_t scratch_bytes, moe_stream_t stream) {
+  if (T > 0 && !hq_scale) return MOE_ERR_INVALID_ARG;
+  if (misaligned(hq_scale, 4)) return MOE_ERR_MISALIGNED;
+  return norm_backward(dy, dh, hq, hq_scale, rstd, weight, weight_dtype, T, H, dx, dweight, scratch,
+                       scratch_bytes, stream);
+}
+
+moe_status_t moe_pack_q8(const void* x, int T, int H, void* xq, float* xq_scale,
+                         moe_stream_t stream) {
+  if (T < 0 || H <= 0 || H % 16 != 0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;  // an empty tensor's pointer may be NULL
+  if (!x || !xq || !xq_scale) return MOE_ERR_INVALID_ARG;
+  if (misaligned(x, 16) || misaligned(xq, 16) || misaligned(xq_scale, 4)) return MOE_ERR_MISALIGNED;
+  return cuda_status(launch_pack_q8(x, T, H, xq, xq_scale, stream));
+}
+
+moe_status_t moe_unpack_q8(const void* xq, const float* xq_scale, int T, int H, void* x,
+                           moe_stream_t stream) {
+  if (T < 0 || H <= 0 || H % 16 != 0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !xq || !xq_scale) return MOE_ERR_INVALID_ARG;
+  if (misaligned(x, 16) || misaligned(xq, 16) || misaligned(xq_scale, 4)) return MOE_ERR_MISALIGNED;
+  return cuda_status(launch_unpack_q8(xq, xq_scale, T, H, x, stream));
+}
+
+moe_status_t moe_experts_backward_scratch_bytes(int T, int H, int E, int K, int I, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const moe_status_t s = check_experts(T, H, E, K, I);
   if (s != MOE_OK) return s;
-  if (!dweight || !scratch) return MOE_ERR_INVALID_ARG;
-  if (T > 0 && (!dy || !h || !rstd || !weight || !dx)) return MOE_ERR_INVALID_ARG;
-  if (scratch_bytes < add_rmsnorm_backward_scratch_bytes(T, H)) return MOE_ERR_WORKSPACE;
-  if (misaligned(dy, 16) || misaligned(dh, 16) || misaligned(h, 16) || misaligned(weight, 16) ||
-      misaligned(dx, 16) || misaligned(rstd, 4) || misaligned(dweight, 4) ||
-      misaligned(scratch, 256))
-    return MOE_ERR_MISALIGNED;
-  return cuda_status(launch_add_rmsnorm_backward(dy, dh, h, rstd, weight,
-                                                 weight_dtype == MOE_DT_F32, T, H, dx, dweight,
-                                                 scratch, stream));
+  *bytes = experts_backward_scratch_bytes(T, H, E, K, I);
+  return MOE_OK;
+}
+
+moe_status_t moe_experts_backward(const void* x, const void* xq, const float* xq_scale,
+                                  const void* dout, const int32_t* offsets,
+                                  const int32_t* row_to_flat, const int32_t* flat_to_row,
+                                  const float* weights, int T, int H, int E, int K, int I,
+                                  const void* w1, const void* w3, const void* w2,
+                                  const void* dx_add, void* dx, float* d_weights, void* dw1,
+                                  void* dw3, void* dw2, int dw_dtype, int accumulate,
+                                  void* scratch, size_t scratch_bytes, int32_t* dev_status,
+                                  moe_stream_t stream) {
+  const moe_status_t s = check_experts(T, H, E, K, I);
+  if (s != MOE_OK) return s;
+  if (dw_dtype != MOE_DT_BF16 && dw_dtype != MOE_DT_F32) return MOE_ERR_INVALID_ARG;
+  if ((accumulate != 0 && accumulate != 1) || (!dw1) != (!dw3) || (!dw1) != (!dw2))
+    return MOE_ERR_INVALID_ARG;
+  if (dw1 && accumulate && dw_dtype != MOE_DT_F32) return MOE_ERR_UNSUPPORTED;
+  if (!offsets || !w1 || !w3 || !w2 || !scratch) return MOE_ERR_INVALID_ARG;
+  if (T > 0) {
+    if ((!x && !xq) || (x && xq) || (xq == nullptr) != (xq_scale == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!dout || !row_to_flat || !flat_to_row || !weights) return MOE_ERR_INVALID_ARG;
+    if (!dx && !d_weights && !dw1) return MOE_ERR_INVALID_ARG;
+  }
+  if (scratch_bytes < experts_backward_scratch_bytes(T, H, E, K, I)) return MOE_ERR_WORKSPACE;
+  for (const void* p : {x, xq, dout, w1, w3, w2, dx_add, (const void*)dx, (const void*)dw1,
+                        (const void*)dw3, (const void*)dw2})
+    if (misaligned(p, 16)) return MOE_ERR_MISALIGNED;
+  for (const void* p : {(const void*)xq_scale, (const void*)offsets, (const void*)row_to_flat,
+                        (const void*)flat_to_row, (const void*)weights, (const void*)d_weights,
+                        (const void*)dev_status})
+    if (misaligned(p, 4)) return MOE_ERR_MISALIGNED;
+  if (misaligned(scratch, 256)) return MOE_ERR_MISALIGNED;
+  if (T == 0 && (!dw1 || accumulate)) return MOE_OK;
+  ExpertsBackwardArgs a{};
+  a.x = x; a.xq = xq; a.xq_scale = xq_scale; a.dout = dout;
+  a.offsets = offsets; a.row_to_flat = row_to_flat; a.flat_to_row = flat_to_row; a.weights = weights;
+  a.T = T; a.H = H; a.E = E; a.K = K; a.I = I;
+  a.w1 = w1; a.w3 = w3; a.w2 = w2; a.dx_add = dx_add; a.dx = dx; a.d_weights = d_weights;
+  a.dw1 = dw1; a.dw3 = dw3; a.dw2 = dw2;
+  a.dw_f32 = dw_dtype == MOE_DT_F32; a.accumulate = accumulate != 0; a.dev_status = dev_status;
+  return cuda_status(launch_experts_backward(a, scratch, stream));
 }
 
 moe_status_t moe_balance_loss_scratch_bytes(int T, int E, int n_seq, size_t* bytes) {

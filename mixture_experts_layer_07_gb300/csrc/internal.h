@@ -184,10 +184,37 @@ cudaError_t launch_add_rmsnorm(const void* x, const void* residual, const void* 
                                int H, float eps, void* h, void* y, float* rstd, void* yq,
                                float* yscale, int q_group, cudaStream_t stream);
 size_t add_rmsnorm_backward_scratch_bytes(int T, int H);
+// hscale: h is e4m3 codes with these scales per row and 128 columns; NULL: bf16
 cudaError_t launch_add_rmsnorm_backward(const void* dy, const void* dh, const void* h,
-                                        const float* rstd, const void* w, bool w32, int T, int H,
-                                        void* dx, float* dweight, void* scratch,
-                                        cudaStream_t stream);
+                                        const float* hscale, const float* rstd, const void* w,
+                                        bool w32, int T, int H, void* dx, float* dweight,
+                                        void* scratch, cudaStream_t stream);
+
+// Rows as e4m3 codes with a scale per row and 128 columns, and back (pack_q8.cu).
+cudaError_t launch_pack_q8(const void* x, int T, int H, void* xq, float* scale, cudaStream_t stream);
+cudaError_t launch_unpack_q8(const void* xq, const float* scale, int T, int H, void* x,
+                             cudaStream_t stream);
+
+// Gradient of sort, experts and weighted return (experts_grad.cu).
+struct ExpertsBackwardArgs {
+  const void* x;         // bf16 tokens, or NULL with
+  const void* xq;        // their e4m3 codes and scales per 128 columns
+  const float* xq_scale;
+  const void* dout;
+  const int32_t *offsets, *row_to_flat, *flat_to_row;
+  const float* weights;
+  int T, H, E, K, I;
+  const void *w1, *w3, *w2;
+  const void* dx_add;  // nullable
+  void* dx;            // nullable
+  float* d_weights;    // nullable
+  void *dw1, *dw3, *dw2;  // nullable together
+  bool dw_f32, accumulate;
+  int32_t* dev_status;
+};
+size_t experts_backward_scratch_bytes(int T, int H, int E, int K, int I);
+cudaError_t launch_experts_backward(const ExpertsBackwardArgs& a, void* scratch,
+                                    cudaStream_t stream);
 
 // Router losses and gradient (route_grad.cu).  The losses' scratch must be
 // zero before the first call and is zero again after each.

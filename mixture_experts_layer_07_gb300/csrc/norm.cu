@@ -19,15 +19,15 @@
 // and a scale per row 79.7 us, 99 % of the copy rate; T = 4096, H = 2880 with a
 // scale per 128 columns 20.8 us (77 %, 1.7 us of it the launch); T = 1, H = 2048
 // 1.7 us.  Backward T = 8192, H = 7168 75.6 us (93 %).
-#include <cuda_fp8.h>
-
 #include "common.cuh"
+#include "e4m3.cuh"
 #include "f32x2.cuh"
 #include "internal.h"
 #include "sm100_ptx.cuh"
 
 namespace {
 
+using namespace moe_e4m3;
 using namespace moe_f32x2;
 
 constexpr int kMaxWarps = 32;
@@ -103,48 +103,6 @@ MOE_DEVICE void load_weight8(const void* w, int vec, float* f) {
   } else {
     bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(w) + vec), f);
   }
-}
-
-MOE_DEVICE uint4 pack8(const float* f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
-
-MOE_DEVICE uint32_t amax8(const float* f) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(f[q]) & 0x7fffffffu);
-  return m;
-}
-
-// Eight e4m3 codes of f / sc (0 where the whole group is zero).  The quotients
-// are IEEE's: with r = RN(1 / sc) and q = RN(f r), RN(q + r (f - q sc)) is the
-// correctly rounded quotient (Markstein's theorem) while nothing leaves the
-// normal range, which scales within 2^+-80 see to -- |f / sc| is at most 448.
-// Three operations per value where the division takes about ten.
-MOE_DEVICE uint2 codes8(const float* f, float sc) {
-  if (sc == 0.f) return make_uint2(0u, 0u);
-  float q[8];
-  if (sc > 0x1p-80f && sc < 0x1p80f) {
-    const float r = __frcp_rn(sc);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q0 = f[i] * r;
-      q[i] = fmaf(fmaf(-q0, sc, f[i]), r, q0);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(f[i], sc);
-  }
-  uint32_t w[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    w[h] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[4 * h], q[4 * h + 1]), __NV_SATFINITE,
-                                              __NV_E4M3) |
-           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[4 * h + 2], q[4 * h + 3]),
-                                              __NV_SATFINITE, __NV_E4M3)
-               << 16;
-  return make_uint2(w[0], w[1]);
 }
 
 enum { kQNone = 0, kQGroup = 1, kQRow = 2 };
@@ -256,10 +214,12 @@ MOE_DEVICE void weight4(const void* w, int vec, float2* f) {
 // fp32 partial row is written.  (T = 8192, H = 7168: rows loaded into registers
 // when their turn comes 88 us; ring of two stages, two vectors per thread 86;
 // four stages, one vector, LAG 78; running offsets 76.)
-template <int VPT, int S, int MAXT, int BPS, bool LAG, bool W32>
+// HQ: h lies as e4m3 codes with a scale per row and 16 vectors; a stage's slot of
+// h then holds a vector's eight codes and, behind them, its scale.
+template <int VPT, int S, int MAXT, int BPS, bool LAG, bool W32, bool HQ>
 __global__ void __launch_bounds__(MAXT, BPS)
-rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restrict__ h,
-                        const float* __restrict__ rstd, const void* __restrict__ w, int T, int H8,
+rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const void* __restrict__ h,
+                        const float* __restrict__ hscale, const float* __restrict__ rstd, const void* __restrict__ w, int T, int H8,
                         float inv_h, int tpr, uint4* dx, float* __restrict__ part) {
   constexpr int kAhead = LAG ? S - 2 : S - 1;  // groups in flight behind the current one
   extern __shared__ uint4 ring[];              // [S][3][VPT][blockDim.x]
@@ -287,13 +247,30 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restric
         if (lt + tpr * j >= H8) continue;
         const size_t o = o_issue + tpr * j;
         moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 0, j)), dy + o, 16);
-        moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 1, j)), h + o, 16);
+        if constexpr (HQ) {
+          const uint32_t to = moe_ptx::smem_u32(slot_of(st, 1, j));
+          moe_ptx::cp_async_8(to, static_cast<const uint2*>(h) + o);
+          moe_ptx::cp_async_4(to + 8, hscale + (size_t)t_issue * ((H8 + 15) >> 4) + ((lt + tpr * j) >> 4), 4);
+        } else {
+          moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 1, j)), static_cast<const uint4*>(h) + o, 16);
+        }
         if (dh) moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 2, j)), dh + o, 16);
       }
     }
     moe_ptx::cp_async_commit();
     t_issue += rows;
     o_issue += hop;
+  };
+  // h of vector j in stage st
+  auto load_h = [&](int st, int j, float2* f) {
+    const uint4 v = *slot_of(st, 1, j);
+    if constexpr (HQ) {
+      codes4(make_uint2(v.x, v.y), f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f[q] = mul2(f[q], pair(__uint_as_float(v.z)));
+    } else {
+      unpack4(v, f);
+    }
   };
   auto row_rstd = [&](uint32_t t) { return t < (uint32_t)T ? __ldg(rstd + t) : 0.f; };
   constexpr bool kKeepW = VPT == 1;  // the weight stays in registers where they suffice
@@ -318,7 +295,7 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restric
       if (lt + tpr * j >= H8 || t_done >= (uint32_t)T) continue;
       float2 gf[4], hf[4], wf[4], ef[4], o[4];
       unpack4(*slot_of(st, 0, j), gf);
-      unpack4(*slot_of(st, 1, j), hf);
+      load_h(st, j, hf);
       unpack4(dh ? *slot_of(st, 2, j) : make_uint4(0u, 0u, 0u, 0u), ef);
       if constexpr (!kKeepW) weight4<W32>(w, lt + tpr * j, wf);
 #pragma unroll
@@ -348,7 +325,7 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const uint4* __restric
         if (lt + tpr * j >= H8) continue;
         float2 gf[4], hf[4], wf[4];
         unpack4(*slot_of(st, 0, j), gf);
-        unpack4(*slot_of(st, 1, j), hf);
+        load_h(st, j, hf);
         if constexpr (!kKeepW) weight4<W32>(w, lt + tpr * j, wf);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -488,21 +465,40 @@ cudaError_t run_norm_q(int q, bool w32, const RowShape& r, const NormArgs& a, cu
                       : run_norm<VPT, kQNone>(w32, r, a, s);
 }
 
-template <int VPT, int S, int MAXT, int BPS, bool LAG>
-cudaError_t run_backward(bool w32, const BackShape& r, const void* dy, const void* dh,
-                         const void* h, const float* rstd, const void* w, int T, int H, void* dx,
-                         float* part, cudaStream_t stream) {
-  auto k = w32 ? rmsnorm_backward_kernel<VPT, S, MAXT, BPS, LAG, true>
-               : rmsnorm_backward_kernel<VPT, S, MAXT, BPS, LAG, false>;
+struct BackArgs {
+  const void *dy, *dh, *h;
+  const float* hscale;  // h as codes, or NULL
+  const float* rstd;
+  const void* w;
+  int T, H;
+  void* dx;
+  float* part;
+};
+
+template <int VPT, int S, int MAXT, int BPS, bool LAG, bool HQ>
+cudaError_t run_backward(bool w32, const BackShape& r, const BackArgs& a, cudaStream_t stream) {
+  auto k = w32 ? rmsnorm_backward_kernel<VPT, S, MAXT, BPS, LAG, true, HQ>
+               : rmsnorm_backward_kernel<VPT, S, MAXT, BPS, LAG, false, HQ>;
   constexpr size_t kPerThread = (size_t)S * 3 * VPT * 16;  // >= 32 VPT: the rows' sums fit
   static std::atomic<unsigned long long> set[2];
   cudaError_t e = moe_raise_smem(k, kPerThread * MAXT, set[w32]);
   if (e != cudaSuccess) return e;
   const int threads = r.tpr * r.rpb;
   return moe_launch(k, dim3(r.grid), dim3(threads), kPerThread * threads, stream, 1,
-                    static_cast<const uint4*>(dy), static_cast<const uint4*>(dh),
-                    static_cast<const uint4*>(h), rstd, w, T, H / 8, 1.f / (float)H, r.tpr,
-                    static_cast<uint4*>(dx), part);
+                    static_cast<const uint4*>(a.dy), static_cast<const uint4*>(a.dh), a.h, a.hscale,
+                    a.rstd, a.w, a.T, a.H / 8, 1.f / (float)a.H, r.tpr, static_cast<uint4*>(a.dx),
+                    a.part);
+}
+
+template <bool HQ>
+cudaError_t run_backward_of(bool w32, const BackShape& r, const BackArgs& a, cudaStream_t s) {
+  switch (r.vpt) {  // 196 KB of ring per SM each
+    case 1:
+      return a.H <= 4096 ? run_backward<1, 4, 512, 2, true, HQ>(w32, r, a, s)
+                         : run_backward<1, 4, 1024, 1, true, HQ>(w32, r, a, s);
+    case 4: return run_backward<4, 2, 512, 1, false, HQ>(w32, r, a, s);
+    default: return run_backward<8, 1, 512, 1, false, HQ>(w32, r, a, s);
+  }
 }
 
 }  // namespace
@@ -527,24 +523,17 @@ size_t add_rmsnorm_backward_scratch_bytes(int T, int H) {
 }
 
 cudaError_t launch_add_rmsnorm_backward(const void* dy, const void* dh, const void* h,
-                                        const float* rstd, const void* w, bool w32, int T, int H,
-                                        void* dx, float* dweight, void* scratch,
-                                        cudaStream_t stream) {
+                                        const float* hscale, const float* rstd, const void* w,
+                                        bool w32, int T, int H, void* dx, float* dweight,
+                                        void* scratch, cudaStream_t stream) {
   float* part = static_cast<float*>(scratch);
   int rows = 0;
   if (T > 0) {
     const BackShape r = back_shape(T, H / 8);
     rows = r.grid;
-    cudaError_t e;
-    switch (r.vpt) {  // 196 KB of ring per SM each
-      case 1:
-        e = H <= 4096
-                ? run_backward<1, 4, 512, 2, true>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream)
-                : run_backward<1, 4, 1024, 1, true>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream);
-        break;
-      case 4: e = run_backward<4, 2, 512, 1, false>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream); break;
-      default: e = run_backward<8, 1, 512, 1, false>(w32, r, dy, dh, h, rstd, w, T, H, dx, part, stream);
-    }
+    const BackArgs a{dy, dh, h, hscale, rstd, w, T, H, dx, part};
+    const cudaError_t e =
+        hscale ? run_backward_of<true>(w32, r, a, stream) : run_backward_of<false>(w32, r, a, stream);
     if (e != cudaSuccess) return e;
   }
   return moe_launch(column_sum_kernel, dim3(moe_cdiv(H, 32)), dim3(1024), 0, stream, 1,

@@ -23,6 +23,10 @@ MOE_DEVICE void cp_async_4(uint32_t dst, const void* src, int src_bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
                : "memory");
 }
+// 8-byte cp.async
+MOE_DEVICE void cp_async_8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 MOE_DEVICE void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 MOE_DEVICE void cp_async_wait() {
@@ -106,6 +110,35 @@ MOE_DEVICE void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, 
       : "memory");
 }
 
+// Tile stores from shared memory (128-byte-swizzled as the loads land it); parts
+// of the box outside the tensor are left out.  A thread's stores form bulk groups:
+// commit, then wait until their shared memory is read, or until they are done.
+MOE_DEVICE void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+// the same, adding to what the tensor holds (in the tensor's type)
+MOE_DEVICE void tma_reduce_add_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::
+          "l"(reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+MOE_DEVICE void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+MOE_DEVICE void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+MOE_DEVICE void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// this thread's writes to shared memory -> later reads by TMA or the tensor core
+MOE_DEVICE void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 MOE_DEVICE void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -179,6 +212,21 @@ MOE_DEVICE uint64_t sdesc_k128_sw128(uint32_t saddr) {
   d |= static_cast<uint64_t>(2) << 61;                   // bits 61-63 128-byte swizzle
   return d;
 }
+
+// The same for an MN-major tile: panels of 64 bf16 along M or N (128-byte rows, one
+// per K index, 128-byte swizzle: 8 K rows per 1024-byte group), `panel` bytes apart.
+// 16 K rows on lie 2048 bytes further.
+MOE_DEVICE uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t panel) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(panel >> 4) << 16;  // leading offset: the next 64 of M or N
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;   // stride offset: the next 8 of K
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+constexpr uint32_t kIdescMnA = 1u << 15;  // A is MN-major
+constexpr uint32_t kIdescMnB = 1u << 16;  // B is MN-major
 
 // Instruction descriptor, kind::f16: D fp32, A and B bf16, both K-major.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {

@@ -40,7 +40,9 @@ EXPORTS = ["moe_status_string", "moe_default_m_skinny", "moe_block_variant", "mo
            "moe_router_tc_scratch_bytes", "moe_router_gemm_tc", "moe_bounded_wait_check",
            "moe_add_rmsnorm", "moe_add_rmsnorm_backward_scratch_bytes",
            "moe_add_rmsnorm_backward", "moe_balance_loss_scratch_bytes", "moe_balance_loss",
-           "moe_route_backward", "moe_unpermute_backward", "moe_layer_q8"]
+           "moe_route_backward", "moe_unpermute_backward", "moe_layer_q8", "moe_pack_q8",
+           "moe_unpack_q8", "moe_add_rmsnorm_backward_q8", "moe_experts_backward_scratch_bytes",
+           "moe_experts_backward"]
 
 PERMUTE_STATIC_SCRATCH_BYTES = 1 << 20
 DT_BF16, DT_F32 = 0, 1
@@ -126,6 +128,12 @@ def _lib():
             "moe_route_backward": [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P,
                                    _P, _I, _P, _P],
             "moe_unpermute_backward": [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P],
+            "moe_pack_q8": [_P, _I, _I, _P, _P, _P],
+            "moe_unpack_q8": [_P, _P, _I, _I, _P, _P],
+            "moe_add_rmsnorm_backward_q8": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _S, _P],
+            "moe_experts_backward_scratch_bytes": [_I, _I, _I, _I, _I, ctypes.POINTER(_S)],
+            "moe_experts_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P,
+                                     _P, _P, _P, _P, _P, _P, _I, _I, _P, _S, _P, _P],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -149,7 +157,8 @@ def binding():
         spec.loader.exec_module(module)
         module.connect(*[ctypes.cast(getattr(_lib(), "moe_" + n), _P).value for n in
                          ("add_rmsnorm", "add_rmsnorm_backward", "balance_loss",
-                          "route_backward", "unpermute_backward")])
+                          "route_backward", "unpermute_backward", "pack_q8", "unpack_q8",
+                          "add_rmsnorm_backward_q8", "experts_backward")])
         _B = module
     return _B
 
@@ -361,6 +370,41 @@ def unpermute_backward(dout, flat_to_row, weights, T, K, H, *, y=None, dy=None, 
     _check(binding().unpermute_backward(dout, flat_to_row, weights, T, K, H, y, dy, d_weights,
                                       shared_y, shared_gate, d_shared_y, d_shared_gate, stream),
            "moe_unpermute_backward")
+
+
+def pack_q8(x, xq, xq_scale, stream=None):
+    """Rows of x as e4m3 codes with a scale per 128 columns, to be kept for the backward pass."""
+    _check(binding().pack_q8(x, xq, xq_scale, stream), "moe_pack_q8")
+
+
+def unpack_q8(xq, xq_scale, x, stream=None):
+    """x = the bf16 rows that the codes stand for."""
+    _check(binding().unpack_q8(xq, xq_scale, x, stream), "moe_unpack_q8")
+
+
+def add_rmsnorm_backward_q8(dy, hq, hq_scale, rstd, weight, dx, dweight, scratch, *, dh=None,
+                            stream=None):
+    """add_rmsnorm_backward (and its scratch) with h kept as pack_q8's codes."""
+    _check(binding().add_rmsnorm_backward_q8(dy, hq, hq_scale, rstd, weight, dx, dweight, scratch, dh,
+                                             stream), "moe_add_rmsnorm_backward_q8")
+
+
+def experts_backward_scratch_bytes(T: int, H: int, E: int, K: int, I: int) -> int:
+    n = _S()
+    _check(_lib().moe_experts_backward_scratch_bytes(T, H, E, K, I, ctypes.byref(n)),
+           "moe_experts_backward_scratch_bytes")
+    return n.value
+
+
+def experts_backward(dout, offsets, row_to_flat, flat_to_row, weights, w1, w3, w2, scratch, *,
+                     x=None, xq=None, xq_scale=None, dx_add=None, dx=None, d_weights=None, dw1=None,
+                     dw3=None, dw2=None, accumulate=False, dev_status=None, stream=None):
+    """Gradients of permute, grouped_gemm and unpermute as one, from the tokens (x, or xq and
+    xq_scale), the routing and dout: dx, d_weights and dw1, dw3, dw2 (bf16 or fp32; accumulate
+    adds to them), each where given; see the header."""
+    _check(binding().experts_backward(dout, offsets, row_to_flat, flat_to_row, weights, w1, w3, w2,
+                                      scratch, x, xq, xq_scale, dx_add, dx, d_weights, dw1, dw3, dw2,
+                                      int(accumulate), dev_status, stream), "moe_experts_backward")
 
 
 def _check_tensors(*specs):

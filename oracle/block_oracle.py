@@ -150,3 +150,65 @@ def unpermute_backward(dout, y, flat_to_row, weights, shared_y=None, shared_gate
         out["d_shared_y"] = np.asarray(shared_gate, np.float64)[:, None] * dout
         out["d_shared_gate"] = (dout * np.asarray(shared_y, np.float64)).sum(axis=1)
     return out
+
+
+def pack_q8(x):
+    """(values / scale before their rounding to e4m3, scales) per row and 128 columns."""
+    x = np.asarray(x, np.float64)
+    s = group_scales(x, 128)
+    wide = np.repeat(s, 128, axis=1)[:, :x.shape[1]]
+    return np.divide(x, wide, out=np.zeros_like(x), where=wide > 0), s
+
+
+def experts_backward(x, dout, ids, weights, w1, w3, w2, errors=None):
+    """Gradients of out[t] = sum_k weights[t, k] W2[e] (silu(W1[e] x_t) * (W3[e] x_t)), e = ids[t, k]
+    (below 0: dropped): dict(dx, d_weights, dw1, dw3, dw2).
+
+    errors = (u, b): the same dict holds, under "e_" + name, how far a computation may be off
+    whose matrix products sum in fp32 (half step u) and round dg, du, weights * act to bf16
+    (half step b); the outputs' own rounding is not in it.
+    """
+    x, dout, weights = (np.asarray(a, np.float64) for a in (x, dout, weights))
+    T, K = ids.shape
+    E, I, H = w1.shape
+    u, b = errors or (0.0, 0.0)
+    out = {"dx": np.zeros((T, H)), "d_weights": np.zeros((T, K)), "dw1": np.zeros((E, I, H)),
+           "dw3": np.zeros((E, I, H)), "dw2": np.zeros((E, H, I))}
+    err = {k: np.zeros_like(v) for k, v in out.items()}
+    # the error of a sum of n products: an addition for each 8 of them (and some for a step's
+    # own alignment), each off by a step at most
+    dot = lambda n: (n / 4 + 64) * u  # noqa: E731
+    for e in range(E):
+        t, k = np.nonzero(ids == e)
+        if not len(t):
+            continue
+        m1, m3, m2 = (np.asarray(m[e], np.float64) for m in (w1, w3, w2))
+        xe, de, w = x[t], dout[t], weights[t, k][:, None]
+        g, up, a = xe @ m1.T, xe @ m3.T, de @ m2
+        s = 1.0 / (1.0 + np.exp(-g))
+        h, f = g * s, s * (1 + g * (1 - s))
+        dg, du, act = w * a * up * f, w * a * h, w * h * up
+        out["d_weights"][t, k] = (a * h * up).sum(axis=1)
+        np.add.at(out["dx"], t, dg @ m1 + du @ m3)
+        out["dw1"][e], out["dw3"][e], out["dw2"][e] = dg.T @ xe, du.T @ xe, de.T @ act
+        if errors is None:
+            continue
+        A = np.abs
+        # of the recomputed products; |silu'| <= 1.1, |silu''| <= 0.5; 2^-18 for exp and the few
+        # products around it
+        eg, eu, ea = dot(H) * (A(xe) @ A(m1).T), dot(H) * (A(xe) @ A(m3).T), dot(H) * (A(de) @ A(m2))
+        near, c = 2.0 ** -18, b + 2.0 ** -18
+        edg = A(w) * (A(up * f) * ea + A(a * f) * eu + 0.5 * A(a * up) * eg
+                      + near * A(a * up) * (s + A(h))) + c * A(dg)
+        edu = A(w) * (A(h) * ea + 1.1 * A(a) * eg) + c * A(du)
+        eact = A(w) * (A(h) * eu + 1.1 * A(up) * eg) + c * A(act)
+        err["d_weights"][t, k] = (A(h * up) * ea + A(a) * (A(h) * eu + 1.1 * A(up) * eg)
+                                  + 2 * near * A(a * h * up)).sum(axis=1)
+        np.add.at(err["dx"], t, edg @ A(m1) + edu @ A(m3) + dot(2 * I) * (A(dg) @ A(m1) + A(du) @ A(m3)))
+        n = dot(len(t))
+        err["dw1"][e] = edg.T @ A(xe) + n * (A(dg).T @ A(xe))
+        err["dw3"][e] = edu.T @ A(xe) + n * (A(du).T @ A(xe))
+        err["dw2"][e] = A(de).T @ eact + n * (A(de).T @ A(act))
+    if errors is not None:
+        out |= {"e_" + k: v for k, v in err.items()}
+    return out
