@@ -103,11 +103,12 @@ static inline int moe_row_vectors(int H8) {
 MOE_DEVICE void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 MOE_DEVICE void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// cudaLaunchKernelEx with programmatic stream serialisation (and an optional
-// cluster of `cluster_z` CTAs along z).
+// cudaLaunchKernelEx with programmatic stream serialisation, in clusters where
+// `cluster` has more than one CTA.
 template <typename... KArgs, typename... Args>
-static inline cudaError_t moe_launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                                     cudaStream_t stream, int cluster_z, Args&&... args) {
+static inline cudaError_t moe_launch_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                                              size_t smem, cudaStream_t stream, dim3 cluster,
+                                              Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -118,16 +119,23 @@ static inline cudaError_t moe_launch(void (*kernel)(KArgs...), dim3 grid, dim3 b
   attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[n].val.programmaticStreamSerializationAllowed = 1;
   ++n;
-  if (cluster_z > 1) {
+  if (cluster.x * cluster.y * cluster.z > 1) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = 1;
-    attr[n].val.clusterDim.y = 1;
-    attr[n].val.clusterDim.z = cluster_z;
+    attr[n].val.clusterDim.x = cluster.x;
+    attr[n].val.clusterDim.y = cluster.y;
+    attr[n].val.clusterDim.z = cluster.z;
     ++n;
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+// the same with a cluster of `cluster_z` CTAs along z
+template <typename... KArgs, typename... Args>
+static inline cudaError_t moe_launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                     cudaStream_t stream, int cluster_z, Args&&... args) {
+  return moe_launch_clusters(kernel, grid, block, smem, stream, dim3(1, 1, cluster_z),
+                             std::forward<Args>(args)...);
 }
 
 // Raises `kernel`'s dynamic shared-memory limit to `bytes` on the current

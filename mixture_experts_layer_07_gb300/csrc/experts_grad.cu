@@ -11,22 +11,29 @@
 // alone, and <a, act> in place of <dout, y> makes the experts' output rows unneeded.
 //
 // Launches:
-//   rows    the experts' rows of x (bf16, or e4m3 codes decoded to bf16) and of dout,
-//           each expert's starting at a whole 128-row tile, zeros up to a whole 64 rows
-//   part 0  per tile and 128 columns of I: a, g, u in TMEM; writes dg, du, w act
-//           (bf16) and the columns' share of <a, act>
-//   part 2  per expert: its three matrices' gradients, K = its rows (zeros behind them)
-//   part 1  per tile and 256 columns of H: dg W1 + du W3 in fp32, over x's and dout's rows
+//   rows    the experts' rows of x (bf16, or e4m3 codes decoded to bf16) and of dout in
+//           the experts' order, zeros up to a whole 16 rows (the MMA's K)
+//   part 0  per up to 128 rows and 256 columns of I: a, g, u; writes dg, du, w act (bf16)
+//           and each 128 columns' share of <a, act>
+//   part 2  per expert: its three matrices' gradients, K = its rows
+//   part 1  per up to 256 rows and 256 columns of H: dg W1 + du W3 in fp32, over x's and
+//           dout's rows
 //   finish  per token: the K rows' sum, and the shares of <a, act> added in order
-// The products are one kernel: 128 x 256 tiles (tcgen05, 1 CTA per SM, persistent),
-// a ring of 64-deep stages filled by TMA, accumulators in TMEM double buffered so that
-// the epilogue of a unit runs under the next one's products.  Operands that the sums
-// run across the rows of (W2 in a; W1, W3 in dx; both in the matrices' gradients) are
-// read MN-major, as they lie.
+// The products are one kernel: 256 x N tiles by pairs of CTAs (tcgen05, cta_group::2, one
+// CTA per SM, persistent), a ring of 64-deep stages filled by TMA, accumulators in TMEM.
+// In parts 0 and 1 the tile's 256 are weight rows (features) and N the tokens, so that an
+// expert with few rows takes a narrow tile.  Operands that the sums run across the rows of
+// (W2 in a; W1, W3 in dx; both in the matrices' gradients) are read MN-major, as they lie.
+// A pair, because each SM then loads half of B only: with single CTAs and 128 x 256 tiles
+// the loads' 64 bytes per clock and SM were the bound (61 of them in part 0; T = 4096,
+// H = I = 2880, E = 32, K = 4: part 0 773 us, part 1 460, part 2 934).
 //
 // Roundings: dg, du and w act to bf16 (the tensor cores' operands), the outputs once.
-// Everything else is fp32.  No atomics: sums have an order that the sizes and the
-// routing fix.
+// Everything else is fp32.  The tensor cores cut what falls off an fp32 sum, which
+// shortens it by about 10^-8 per K of 16; a, g and u, whose errors d_weights shows (its
+// fp32 is not behind a rounding to bf16), are therefore taken out of TMEM every 256 of K
+// and added in registers (d_weights at H = 2880: 9e-6 off in one go).  No atomics: sums
+// have an order that the sizes and the routing fix.
 #include <cuda.h>
 
 #include "common.cuh"
@@ -43,32 +50,40 @@ using namespace moe_ptx;
 constexpr uint64_t kWaitNs = 2000000000ull;  // every wait gives up after 2 s
 constexpr int kMaxE = 1024;
 
+// Tokens of a tile, at most; a tile of the gradient of x is wider, as it has one
+// accumulator where part 0 has three.
+constexpr int kActTokens = 128, kDxTokens = 256;
+
 // What `rows` writes for the later launches, at the start of the scratch.
 struct Plan {
-  int32_t tiles;
-  int32_t pad[63];
-  int32_t row0[kMaxE];   // an expert's first row in the padded order (a multiple of 128)
-  int32_t count[kMaxE];  // its rows
+  int32_t tiles[2];  // of part 0 and of part 1
+  int32_t pad[62];
+  int2 rows[kMaxE];  // an expert's first row in the padded order (a multiple of 16), its rows
 };
+// The tiles of an expert follow one another; each names the expert, the first of its
+// tiles, the expert's first row and its rows.
+using Tile = int4;
 
 // Where things lie in the scratch.
 struct Layout {
-  long long Rp;  // padded rows: at most R + 127 per expert that has any
-  size_t tile, place, weight, share, rows, act, total;
+  long long Rp;  // padded rows: at most R + 15 per expert that has any
+  size_t tile[2], place, weight, share, rows, act, total;
   int shares;
 };
 Layout layout_of(long long R, int H, int E, int I) {
   Layout l;
-  const long long most = R + 127 * (R < E ? R : E);
-  l.Rp = most < 128 ? 128 : most / 128 * 128;
-  l.shares = 2 * moe_cdiv(I, 128);
+  const long long some = R < E ? R : E;  // experts with rows, at most
+  const long long most = R + 15 * some;
+  l.Rp = most < 16 ? 16 : most / 16 * 16;
+  l.shares = 2 * moe_cdiv(I, 256);
   size_t off = sizeof(Plan);
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = moe_align_up(off + bytes, 1024);
     return o;
   };
-  l.tile = take((size_t)(l.Rp / 128) * 8);
+  l.tile[0] = take((size_t)(R / kActTokens + some + 1) * sizeof(Tile));
+  l.tile[1] = take((size_t)(R / kDxTokens + some + 1) * sizeof(Tile));
   l.place = take((size_t)R * 4);
   l.weight = take((size_t)l.Rp * 4);
   l.share = take((size_t)l.shares * l.Rp * 4);
@@ -87,7 +102,7 @@ struct RowArgs {
   const float* weights;
   int R, H, E, K;
   Plan* plan;
-  int2* tile;
+  Tile* tile[2];
   int32_t* place;
   float* weight;
   uint4 *xp, *dp;
@@ -120,30 +135,45 @@ rows_kernel(const RowArgs a) {
     if (lane_id() == 0) before = 0;
     for (int e = lo; e < hi; ++e) first[e] = max(first[e], before);
     __syncwarp();
-    int s = 0;
-    for (int e = lo; e < min(hi, E); ++e) s += (first[e + 1] - first[e] + 127) & ~127;
-    int sum = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane_id() >= o) sum += v;
+    // sums over the experts before: padded rows, tiles of either kind
+    int s[3] = {0, 0, 0};
+    for (int e = lo; e < min(hi, E); ++e) {
+      const int n = first[e + 1] - first[e];
+      s[0] += (n + 15) & ~15;
+      s[1] += moe_cdiv(n, kActTokens);
+      s[2] += moe_cdiv(n, kDxTokens);
     }
-    s = sum - s;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      int sum = s[i];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane_id() >= o) sum += v;
+      }
+      s[i] = sum - s[i];
+    }
     for (int e = lo; e < hi; ++e) {
-      at[e] = s;
-      if (e < E) s += (first[e + 1] - first[e] + 127) & ~127;
+      at[e] = s[0];
+      if (e == E) {
+        if (blockIdx.x == 0) {
+          a.plan->tiles[0] = s[1];
+          a.plan->tiles[1] = s[2];
+        }
+        break;
+      }
+      const int n = first[e + 1] - first[e];
+      if (blockIdx.x == 0) {
+        a.plan->rows[e] = make_int2(s[0], n);
+        for (int j = 0; j < moe_cdiv(n, kActTokens); ++j) a.tile[0][s[1] + j] = make_int4(e, s[1], s[0], n);
+        for (int j = 0; j < moe_cdiv(n, kDxTokens); ++j) a.tile[1][s[2] + j] = make_int4(e, s[2], s[0], n);
+      }
+      s[0] += (n + 15) & ~15;
+      s[1] += moe_cdiv(n, kActTokens);
+      s[2] += moe_cdiv(n, kDxTokens);
     }
   }
   __syncthreads();
-  if (blockIdx.x == 0) {
-    if (threadIdx.x == 0) a.plan->tiles = at[E] / 128;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-      const int n = first[e + 1] - first[e];
-      a.plan->row0[e] = at[e];
-      a.plan->count[e] = n;
-      for (int j = 0; j < n; j += 128) a.tile[(at[e] + j) / 128] = make_int2(e, min(128, n - j));
-    }
-  }
   // a warp takes half of a padded row's copies: x's or dout's
   const int H8 = a.H / 8, lane = lane_id();
   const int warps = gridDim.x * (blockDim.x / 32);
@@ -158,7 +188,6 @@ rows_kernel(const RowArgs a) {
       e = lo;
     }
     const int i = p - at[e], n = first[e + 1] - first[e];
-    if (i >= ((n + 63) & ~63)) continue;  // no sum reaches these rows
     int flat = -1;
     if (i < n) {
       const int row = first[e] + i;
@@ -189,88 +218,114 @@ rows_kernel(const RowArgs a) {
 // ---------------------------------------------------------------- products
 enum { kAct = 0, kDx = 1, kDw = 2 };  // the launches' parts
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;
-constexpr int kABytes = kBM * kBK * 2, kPanel = 64 * kBK * 2;  // a panel: 64 of M or N, 64 of K
-constexpr int kStageBytes = kABytes + kBN * kBK * 2;
-constexpr int kStages = 4;
-constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, splitting the columns
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kBoxBytes = 32 * 128;  // an epilogue warp's staging: 32 rows of 128 bytes
-constexpr int kNumBars = 2 * kStages + 2 + 3 + 1;
-constexpr size_t kSmemBytes =
-    1024 + (size_t)kStages * kStageBytes + kEpiWarps * kBoxBytes + kNumBars * 8 + 16;
-static_assert(kSmemBytes <= 232448, "227 KB of shared memory per CTA");
+constexpr int kBM = 256, kBK = 64;       // a pair's tile rows; a stage's K
+constexpr int kTile = 128 * kBK * 2;     // a CTA's 128 rows (or columns) of an operand, 64 deep
+constexpr int kPanel = 64 * kBK * 2;     // MN-major: 64 of M or N
+constexpr int kChunk = 4;                // kAct: stages between two additions in registers
+constexpr int kEpiWarps = 8;             // two per TMEM lane quarter, splitting the columns
+constexpr int kBoxBytes = 32 * 128;      // kDw: an epilogue warp's store, 32 rows of 128 bytes
+
+template <int MODE>
+struct Cfg {
+  // kAct: W1, W3 (or W2) and half of 128 tokens; else A and half of 256 columns
+  static constexpr int kStageBytes = MODE == kAct ? 2 * kTile + kTile / 2 : 2 * kTile;
+  static constexpr int kB = MODE == kAct ? 2 * kTile : kTile;  // where B lies in a stage
+  static constexpr int kStages = MODE == kDx ? 6 : 5;
+  // kDw: two boxes per warp; kAct: two sets of the warps' column sums
+  static constexpr int kEpiBytes = MODE == kDw ? 2 * kEpiWarps * kBoxBytes : kEpiWarps * 64 * 4 * 2;
+  static constexpr int kNumBars = 2 * kStages + 3 + 3 + 1 + 2;
+  static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kEpiBytes + kNumBars * 8 + 16;
+  static_assert(kSmemBytes <= 232448, "227 KB of shared memory per CTA");
+};
+constexpr int kThreads = 128 + 32 * kEpiWarps;  // warp 0 TMA, warp 1 MMA, warps 4-11 epilogue
 
 struct GradArgs {
   const Plan* plan;
-  const int2* tile;
+  const Tile* tile[2];
   const float* weight;
   float* share;
+  __nv_bfloat16 *dgu, *act;  // kAct's outputs: [2][Rp][I], [Rp][I]
+  float* rows;               // kDx's: [Rp][H]
   long long Rp;
   int H, I, E;
   int accumulate;
   int32_t* dev_status;
 };
-// A and B of the parts' products and what they store.
-//   kAct: dout's and x's rows | W1, W3, W2 | dg and du, w act
-//   kDx:  dg and du           | W1, W3     | dx's rows
-//   kDw:  dg and du, dout's   | x's, w act | dW1, dW3, dW2
+// A and B of the parts' products, and what kDw stores.
+//   kAct: W1, W3, W2 | x's and dout's rows
+//   kDx:  W1, W3     | dg and du
+//   kDw:  dg and du, dout's rows | x's rows, w act | dW1, dW3, dW2
 struct Maps {
-  CUtensorMap a0, a1, b0, b1, b2, o0, o1, o2;
+  CUtensorMap a0, a1, a2, b0, b1, o0, o1, o2;
 };
 
-// one unit of work: a tile of one expert
+// One unit of work of a pair: a tile of one expert.
 struct Unit {
-  int e, row, m;      // expert, first padded row, rows in use
-  int m0, n0, n;      // the output tile's first row and column, its columns
-  int part, steps;    // which product; 64-deep steps of K
+  int e, row, m;   // expert; kAct, kDx: the tile's first padded row and its tokens; kDw: the expert's
+  int m0, n0, n;   // the tile's first row and column, its columns (a multiple of 16)
+  int part;        // kDw: which matrix
 };
 
+// The units w, w + step, ... of a pair; what a unit needs from memory is loaded while
+// the one before it is worked on.
 template <int MODE>
-MOE_DEVICE Unit unit_of(const GradArgs& a, long long w) {
-  Unit u;
-  if constexpr (MODE == kDw) {
-    const int nI = moe_cdiv(a.I, kBM), nH = moe_cdiv(a.H, kBM);
-    const int wI = moe_cdiv(a.I, kBN), wH = moe_cdiv(a.H, kBN);
-    const int up = nI * wH, per = 2 * up + nH * wI;  // dW1 and dW3 [I, H], dW2 [H, I]
-    u.e = (int)(w / per);
-    int r = (int)(w % per);
-    u.part = r < up ? 0 : r < 2 * up ? 1 : 2;
-    r -= u.part * up;
-    const int wide = u.part == 2 ? wI : wH;
-    u.m0 = r / wide * kBM;
-    u.n0 = r % wide * kBN;
-    u.n = min(kBN, (u.part == 2 ? a.I : a.H) - u.n0);
-    u.row = __ldg(&a.plan->row0[u.e]);
-    u.m = __ldg(&a.plan->count[u.e]);
-    u.steps = (u.m + kBK - 1) / kBK;
-  } else {
-    const int cols = MODE == kAct ? moe_cdiv(a.I, 128) : moe_cdiv(a.H, kBN);
-    const int t = (int)(w / cols);
-    const int2 it = __ldg(a.tile + t);
-    u.e = it.x;
-    u.m = it.y;
-    u.row = t * 128;
-    u.part = 0;
-    u.m0 = 0;
-    u.n0 = (int)(w % cols) * (MODE == kAct ? 128 : kBN);
-    u.n = MODE == kAct ? 128 : min(kBN, a.H - u.n0);
-    u.steps = 2 * moe_cdiv(MODE == kAct ? a.H : a.I, kBK);
+struct Walk {
+  const GradArgs& a;
+  int w, step, total, blocks, up, wI, wH;
+  int4 raw;
+
+  MOE_DEVICE Walk(const GradArgs& g, int first, int by) : a(g), w(first), step(by) {
+    wI = moe_cdiv(a.I, kBM), wH = moe_cdiv(a.H, kBM);
+    up = wI * wH;  // dW1, dW3 and dW2 have as many blocks
+    blocks = MODE == kAct ? wI : MODE == kDx ? wH : 3 * up;
+    total = (MODE == kDw ? a.E : __ldg(&a.plan->tiles[MODE == kDx])) * blocks;
+    load();
   }
-  return u;
-}
-template <int MODE>
-MOE_DEVICE long long units_of(const GradArgs& a) {
-  if constexpr (MODE == kDw)
-    return (long long)a.E * (2 * moe_cdiv(a.I, kBM) * moe_cdiv(a.H, kBN) +
-                             moe_cdiv(a.H, kBM) * moe_cdiv(a.I, kBN));
-  return (long long)__ldg(&a.plan->tiles) * (MODE == kAct ? moe_cdiv(a.I, 128) : moe_cdiv(a.H, kBN));
-}
+  MOE_DEVICE void load() {
+    if (w >= total) return;
+    const int i = (uint32_t)w / (uint32_t)blocks;
+    if constexpr (MODE == kDw) {
+      const int2 r = __ldg(&a.plan->rows[i]);
+      raw = make_int4(i, 0, r.x, r.y);
+    } else {
+      raw = __ldg(a.tile[MODE == kDx] + i);
+    }
+  }
+  MOE_DEVICE bool next(Unit& u) {
+    if (w >= total) return false;
+    u.e = raw.x;
+    u.row = raw.z;
+    u.m = raw.w;
+    u.part = 0;
+    if constexpr (MODE == kDw) {
+      int r = w - u.e * blocks;
+      u.part = r / up;
+      r -= u.part * up;
+      const int wide = u.part == 2 ? wI : wH;
+      u.m0 = r / wide * kBM;
+      u.n0 = r % wide * 256;
+      u.n = min(256, (u.part == 2 ? a.I : a.H) - u.n0);
+    } else {
+      // an expert's tiles of one block follow one another, so its weights are read once
+      constexpr int kMost = MODE == kAct ? kActTokens : kDxTokens;
+      const int tiles = moe_cdiv(u.m, kMost), r = w - raw.y * blocks;
+      const int t = r % tiles, n = (moe_cdiv(u.m, tiles) + 15) & ~15;
+      u.m0 = r / tiles * kBM;
+      u.n0 = 0;
+      u.row += t * n;
+      u.m = min(n, u.m - t * n);
+      u.n = (u.m + 15) & ~15;
+    }
+    w += step;
+    load();
+    return true;
+  }
+};
 
 // A warp's 32 rows x 128 bytes from registers to the tensor: lane's row, as eight
-// 16-byte pieces, through the warp's staging box.
+// 16-byte pieces, through one of the warp's two boxes.
 MOE_DEVICE void box_wait(int lane) {
-  if (lane == 0) bulk_wait_read();  // the last store has read the box
+  if (lane == 0) bulk_wait_read<1>();  // the store before the last one has read its box
   __syncwarp();
 }
 MOE_DEVICE void box_piece(uint8_t* box, int lane, int i, const uint4& v) {
@@ -287,42 +342,76 @@ MOE_DEVICE void box_store(const CUtensorMap* map, const uint8_t* box, int lane, 
   }
 }
 
+// Sums over the warp's lanes of 16 values each; lane 2 i ends up with the sum of value
+// column(2 i).  A lane hands over the half that its partner goes on with.
+MOE_DEVICE float lane_sums16(float (&v)[16], int lane) {
+#pragma unroll
+  for (int o = 16, n = 8; n > 0; o >>= 1, n >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float mine = up ? v[i + n] : v[i], other = up ? v[i] : v[i + n];
+      v[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+MOE_DEVICE int column_of(int lane) {
+  return (lane >> 4 & 1) * 8 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2 + (lane >> 1 & 1);
+}
+
+// Two tokens' values of this lane's feature to two rows of bf16: even lanes store two
+// features of the first token, odd lanes two of the second.
+MOE_DEVICE void store_pair(__nv_bfloat16* row0, int pitch, int feature, int lane, bool in, float v0, float v1) {
+  const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
+  const uint32_t two = lane & 1 ? pack_bf16x2(got, v1) : pack_bf16x2(v0, got);
+  if (in) *reinterpret_cast<uint32_t*>(row0 + (size_t)(lane & 1) * pitch + (feature & ~1)) = two;
+}
+
 // F32: the matrices' gradients in fp32 (kDw), else bf16
 template <int MODE, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
 products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
+  using C = Cfg<MODE>;
+  constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
-  uint8_t* boxes = smem + (size_t)kStages * kStageBytes;
-  uint8_t* bar_area = boxes + kEpiWarps * kBoxBytes;
+  uint8_t* epi = smem + (size_t)kStages * C::kStageBytes;
+  uint8_t* bar_area = epi + C::kEpiBytes;
   const uint32_t bar0 = smem_u32(bar_area);
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };  // the leader's counts for both
   auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
+  // accumulators -- kAct: 0, 1 the two of a, 2 that of g and u; else 0, 1.  empty: the leader's
   auto acc_full = [&](uint32_t i) { return bar0 + 8u * (2 * kStages + i); };
-  // kAct: the two sets of a, and the one of g and u; else the two accumulators
-  auto acc_empty = [&](uint32_t i) { return bar0 + 8u * (2 * kStages + 2 + i); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 5);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 8 * kNumBars);
+  auto acc_empty = [&](uint32_t i) { return bar0 + 8u * (2 * kStages + 3 + i); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 6);
+  auto sums_bar = [&](int half) { return drain_bar + 8u * (1 + half); };  // kAct: the four warps' sums
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 8 * C::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = warp_id(), lane = lane_id();
+  const int warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
+  const uint32_t rank = cluster_rank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(acc_full(i), 1);
-    for (int i = 0; i < 3; ++i) mbar_init(acc_empty(i), 32 * kEpiWarps);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(acc_full(i), 1);
+      mbar_init(acc_empty(i), 2 * kEpiWarps);
+    }
     mbar_init(drain_bar, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(sums_bar(i), 4);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
+    tmem_alloc2(smem_u32(tmem_slot), 512);
+    tmem_relinquish2();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // the pair's barriers are ready
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
@@ -332,243 +421,380 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
     moe_set_status(a.dev_status, MOE_DEV_WAIT_TIMEOUT);
     *abort_flag = 1;
   };
-  const long long total = units_of<MODE>(a);
+  Walk<MODE> walk(a, blockIdx.x >> 1, gridDim.x >> 1);
+  Unit u;
   const int nkH = moe_cdiv(a.H, kBK), nkI = moe_cdiv(a.I, kBK);
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer
+  if (warp < 4) {
+    if constexpr (MODE == kAct) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+      // ---------------- TMA producer (the warp as a whole): this CTA's rows of A, its half of B
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_parity = 0;
       bool ok = true;
-      for (long long w = blockIdx.x; w < total && ok; w += gridDim.x) {
-        const Unit u = unit_of<MODE>(a, w);
-        const int panels = (u.n + 63) / 64;
-        for (int s = 0; s < u.steps; ++s) {
-          if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, kWaitNs)) {
-            fail();
-            ok = false;
-            break;
-          }
-          const uint32_t A = sbase + stage * kStageBytes, B = A + kABytes, bar = full_bar(stage);
-          if constexpr (MODE == kAct) {
-            if (s < nkH) {  // a = dout W2: W2 [H, I] lies MN-major
-              mbar_arrive_expect_tx(bar, kABytes + 2 * kPanel);
-              tma_load_3d(A, &maps.a0, bar, s * kBK, u.row, 0);
-              for (int p = 0; p < 2; ++p)
-                tma_load_3d(B + p * kPanel, &maps.b2, bar, u.n0 + 64 * p, s * kBK, u.e);
-            } else {        // g | u
-              const int k = (s - nkH) * kBK;
-              mbar_arrive_expect_tx(bar, kStageBytes);
-              tma_load_3d(A, &maps.a1, bar, k, u.row, 0);
-              tma_load_3d(B, &maps.b0, bar, k, u.n0, u.e);
-              tma_load_3d(B + kBM * kBK * 2, &maps.b1, bar, k, u.n0, u.e);
-            }
-          } else if constexpr (MODE == kDx) {
-            const int part = s >= nkI, k = (s - part * nkI) * kBK;
-            mbar_arrive_expect_tx(bar, kABytes + panels * kPanel);
-            tma_load_3d(A, &maps.a0, bar, k, u.row, part);
-            for (int p = 0; p < panels; ++p)
-              tma_load_3d(B + p * kPanel, part ? &maps.b1 : &maps.b0, bar, u.n0 + 64 * p, k, u.e);
-          } else {
-            const int row = u.row + s * kBK;
-            mbar_arrive_expect_tx(bar, kABytes + panels * kPanel);
-            for (int p = 0; p < 2; ++p) {
-              if (u.part == 2) tma_load_3d(A + p * kPanel, &maps.a1, bar, u.m0 + 64 * p, row, 0);
-              else tma_load_3d(A + p * kPanel, &maps.a0, bar, u.m0 + 64 * p, row, u.part);
-            }
-            for (int p = 0; p < panels; ++p)
-              tma_load_3d(B + p * kPanel, u.part == 2 ? &maps.b1 : &maps.b0, bar, u.n0 + 64 * p, row, 0);
-          }
-          armed |= 1u << stage;
-          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+      const uint32_t lead = cluster_addr(bar0, 0);
+      uint32_t st = 0, bar = 0;  // the stage being filled and its barrier, in the leader
+      // the next free stage, `bytes` expected in each CTA; whether this lane fills it
+      auto take = [&](int bytes) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, kWaitNs));
+        if (!ok) {
+          fail();
+          return false;
         }
+        st = sbase + stage * C::kStageBytes;
+        bar = lead + 8u * stage;
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        const bool me = elect_one();
+        if (me && rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        return me;
+      };
+      while (ok && walk.next(u)) {
+        const int m0 = u.m0 + 128 * rank, half = u.n / 2;
+        if constexpr (MODE == kAct) {
+          const int row = u.row + half * rank;
+          for (int k0 = 0; k0 < nkH && ok; k0 += kChunk) {
+            const int k1 = min(nkH, k0 + kChunk);
+            for (int k = k0; k < k1 && ok; ++k)  // a = dout W2: W2 [H, I] lies MN-major
+              if (take(kTile + kTile / 2)) {
+                tma_load2_3d(st, &maps.a2, bar, m0, k * kBK, u.e);
+                tma_load2_3d(st + kPanel, &maps.a2, bar, m0 + 64, k * kBK, u.e);
+                tma_load2_3d(st + C::kB, &maps.b1, bar, k * kBK, row, 0);
+              }
+            for (int k = k0; k < k1 && ok; ++k)  // g, u
+              if (take(2 * kTile + kTile / 2)) {
+                tma_load2_3d(st, &maps.a0, bar, k * kBK, m0, u.e);
+                tma_load2_3d(st + kTile, &maps.a1, bar, k * kBK, m0, u.e);
+                tma_load2_3d(st + C::kB, &maps.b0, bar, k * kBK, row, 0);
+              }
+          }
+        } else if constexpr (MODE == kDx) {
+          const int row = u.row + half * rank;
+          const bool two = half > 64;
+          for (int part = 0; part < 2; ++part)  // W1 and W3 [I, H]: MN-major
+            for (int k = 0; k < nkI && ok; ++k)
+              if (take(kTile + (two ? 2 : 1) * kPanel)) {
+                const CUtensorMap* w = part ? &maps.a1 : &maps.a0;
+                tma_load2_3d(st, w, bar, m0, k * kBK, u.e);
+                tma_load2_3d(st + kPanel, w, bar, m0 + 64, k * kBK, u.e);
+                tma_load2_3d(st + C::kB, &maps.b0, bar, k * kBK, row, part);
+                if (two) tma_load2_3d(st + C::kB + kPanel, &maps.b0, bar, k * kBK, row + 64, part);
+              }
+        } else {
+          const int n0 = u.n0 + half * rank, part = u.part == 2 ? 0 : u.part;
+          const bool two = half > 64;
+          const CUtensorMap* ma = u.part == 2 ? &maps.a1 : &maps.a0;
+          const CUtensorMap* mb = u.part == 2 ? &maps.b1 : &maps.b0;
+          for (int r = u.row; r < u.row + u.m && ok; r += kBK)
+            if (take(kTile + (two ? 2 : 1) * kPanel)) {
+              tma_load2_3d(st, ma, bar, m0, r, part);
+              tma_load2_3d(st + kPanel, ma, bar, m0 + 64, r, part);
+              tma_load2_3d(st + C::kB, mb, bar, n0, r, 0);
+              if (two) tma_load2_3d(st + C::kB + kPanel, mb, bar, n0 + 64, r, 0);
+            }
+        }
+        __syncwarp();
       }
-      // every copy this thread started has landed before the CTA moves on
-      for (int s = 0; s < kStages; ++s)
-        if (armed & (1u << s))
-          if (!mbar_wait_bounded(full_bar(s), (armed_parity >> s) & 1u, nullptr, kWaitNs)) fail();
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer
+      // every copy that was started has landed before the pair moves on
+      if (rank == 0) {
+        for (int s = 0; s < kStages; ++s)
+          if (armed & (1u << s))
+            if (!mbar_wait_bounded(full_bar(s), (armed_parity >> s) & 1u, nullptr, kWaitNs)) fail();
+      } else if (!ok) {
+        // given up: the copies count in the leader, so they get their time
+        const uint64_t t0 = globaltimer_ns();
+        for (int i = 0; i < (1 << 20) && globaltimer_ns() - t0 < 1000000; ++i) __nanosleep(1000);
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ---------------- MMA issuer, for the pair (the warp as a whole, one lane issues)
       int stage = 0;
       uint32_t phase = 0, n = 0;
       bool ok = true, issued = false;
-      auto step = [&](uint32_t d, int N, bool mnA, bool mnB, bool first) {
-        if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, kWaitNs)) {
-          fail();
-          return false;
-        }
+      const uint32_t one = sbase >> 4;
+      // the next stage, once it is filled
+      auto filled = [&]() {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(full_bar(stage), phase, abort_flag, kWaitNs));
+        if (!ok) fail();
         tc_fence_after();
-        const uint32_t A = sbase + stage * kStageBytes, B = A + kABytes;
-        const uint32_t id = idesc_bf16_f32(kBM, N) | (mnA ? kIdescMnA : 0u) | (mnB ? kIdescMnB : 0u);
-#pragma unroll
-        for (int k = 0; k < kBK / 16; ++k)
-          tc_mma_f16(d, mnA ? sdesc_mn_sw128(A + k * 2048, kPanel) : sdesc_k128_sw128(A + k * 32),
-                     mnB ? sdesc_mn_sw128(B + k * 2048, kPanel) : sdesc_k128_sw128(B + k * 32), id,
-                     !first || k > 0);
+        return one + stage * (C::kStageBytes >> 4);
+      };
+      auto used = [&]() {
+        if (elect_one()) tc_commit2(empty_bar(stage));
         issued = true;
-        tc_commit(empty_bar(stage));
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
-        return true;
       };
       auto free_acc = [&](uint32_t i, uint32_t use) {  // before the use-th time accumulator i is written
-        if (!mbar_wait_bounded(acc_empty(i), (use & 1u) ^ 1u, abort_flag, kWaitNs)) {
-          fail();
-          return false;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_empty(i), (use & 1u) ^ 1u, abort_flag, kWaitNs));
+        if (!ok) fail();
         tc_fence_after();
-        return true;
       };
-      for (long long w = blockIdx.x; w < total && ok; w += gridDim.x) {
-        const Unit u = unit_of<MODE>(a, w);
-        if (u.steps == 0) continue;
+      auto done = [&](uint32_t i) {
+        if (elect_one()) tc_commit2(acc_full(i));
+      };
+      // descriptors of an operand at 0, and how far 16 of K lie apart (in 16 bytes)
+      const uint64_t dk = sdesc_k128_sw128(0), dmn = sdesc_mn_sw128(0, kPanel);
+      constexpr int kK = 32 >> 4, kMn = 2048 >> 4;
+      while (ok && walk.next(u)) {
+        const uint32_t id = idesc_bf16_f32(kBM, u.n) | (MODE == kDw ? kIdescMnB : 0u);
         if constexpr (MODE == kAct) {
-          ok = free_acc(n & 1u, n >> 1);
-          for (int s = 0; s < nkH && ok; ++s) ok = step(tmem + 128 * (n & 1u), 128, false, true, s == 0);
-          ok = ok && free_acc(2, n);
-          for (int s = 0; s < nkH && ok; ++s) ok = step(tmem + 256, 256, false, false, s == 0);
+          for (int k0 = 0; k0 < nkH && ok; k0 += kChunk, ++n) {
+            const int k1 = min(nkH, k0 + kChunk);
+            free_acc(n & 1u, n >> 1);
+            for (int k = k0; k < k1 && ok; ++k) {
+              const uint32_t A = filled(), d = tmem + 128 * (n & 1u);
+              if (!ok) break;
+              if (elect_one()) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  tc_mma2_f16(d, dmn + A + q * kMn, dk + A + (C::kB >> 4) + q * kK, id | kIdescMnA, k > k0 || q > 0);
+              }
+              used();
+            }
+            if (!ok) break;
+            done(n & 1u);
+            free_acc(2, n);
+            for (int k = k0; k < k1 && ok; ++k) {
+              const uint32_t A = filled();
+              if (!ok) break;
+              if (elect_one()) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const uint64_t b = dk + A + (C::kB >> 4) + q * kK;
+                  tc_mma2_f16(tmem + 256, dk + A + q * kK, b, id, k > k0 || q > 0);
+                  tc_mma2_f16(tmem + 384, dk + A + (kTile >> 4) + q * kK, b, id, k > k0 || q > 0);
+                }
+              }
+              used();
+            }
+            if (!ok) break;
+            done(2);
+          }
         } else {
-          ok = free_acc(n & 1u, n >> 1);
-          for (int s = 0; s < u.steps && ok; ++s)
-            ok = step(tmem + 256 * (n & 1u), u.n, MODE == kDw, true, s == 0);
+          // kDx: all of K; kDw: the expert's rows, the last stage's as far as they go
+          const int k16 = MODE == kDx ? 8 * nkI : (u.m + 15) / 16;
+          if (k16 == 0) continue;
+          const uint32_t d = tmem + 256 * (n & 1u);
+          free_acc(n & 1u, n >> 1);
+          for (int k = 0; k < k16 && ok; k += 4) {
+            const uint32_t A = filled(), B = A + (C::kB >> 4);
+            if (!ok) break;
+            if (elect_one()) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (MODE == kDx || k + q < k16)
+                  tc_mma2_f16(d, dmn + A + q * kMn, MODE == kDw ? dmn + B + q * kMn : dk + B + q * kK,
+                              id | kIdescMnA, k > 0 || q > 0);
+            }
+            used();
+          }
+          if (!ok) break;
+          done(n & 1u);
+          ++n;
         }
-        if (!ok) break;
-        tc_commit(acc_full(n & 1u));
-        ++n;
       }
       if (issued) {
-        // all MMAs of this thread complete before TMEM is released
-        tc_commit(drain_bar);
+        // all MMAs of this warp complete before TMEM is released
+        if (elect_one()) tc_commit2(drain_bar);
         if (!mbar_wait_bounded(drain_bar, 0, nullptr, kWaitNs)) fail();
       }
     }
   } else {
-    // ---------------- epilogue: lane quarter = warp % 4, half of the columns each
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    // ---------------- epilogue: lane quarter = warp % 4, alternate columns for the two of a quarter
+    if constexpr (MODE == kAct) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    uint8_t* box = boxes + (warp - 2) * kBoxBytes;
     uint32_t n = 0;
-    for (long long w = blockIdx.x; w < total; w += gridDim.x) {
-      const Unit u = unit_of<MODE>(a, w);
-      const int r0 = quarter * 32;  // the warp's first row of the tile
-      if (MODE == kDw && u.steps == 0) {
-        // an expert without rows: zeros, or nothing to add
-        const int rows = u.part == 2 ? a.H : a.I;
-        if (a.accumulate || u.m0 + r0 >= rows) continue;
-        box_wait(lane);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) box_piece(box, lane, i, make_uint4(0u, 0u, 0u, 0u));
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          for (int c = half * 128; c < min(u.n, half * 128 + 128); c += F32 ? 32 : 64)
-            tma_store_3d(u.part == 0 ? &maps.o0 : u.part == 1 ? &maps.o1 : &maps.o2, smem_u32(box),
-                         u.n0 + c, u.m0 + r0, u.e);
-          bulk_commit();
-        }
-        __syncwarp();
-        continue;
-      }
-      if (!mbar_wait_bounded(acc_full(n & 1u), (n >> 1) & 1u, abort_flag, kWaitNs)) {
+    bool ok = true;
+    auto wait_acc = [&](uint32_t i, uint32_t use) {
+      if (!mbar_wait_bounded(acc_full(i), use & 1u, abort_flag, kWaitNs)) {
         fail();
-        break;
+        ok = false;
       }
+      ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      if constexpr (MODE == kAct) {
-        const int row = u.row + r0 + lane;
-        const bool in = r0 + lane < u.m;
-        const float wr = in ? __ldg(a.weight + row) : 0.f;
-        uint32_t pg[32], pu[32], pa[32];
-        float share = 0.f;
-        const uint32_t ta = t_lane + 128 * (n & 1u) + 64 * half, tg = t_lane + 256 + 64 * half;
+    };
+    auto release_acc = [&](uint32_t i) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(acc_empty(i), 0));
+    };
+    if constexpr (MODE == kAct) {
+      float* sums = reinterpret_cast<float*>(epi);  // [2][warps][64]
+      for (uint32_t unit = 0; ok && walk.next(u); ++unit) {
+        // a thread's feature; its columns (tokens) 64 half .. + 63
+        const int i = u.m0 + 128 * rank + 32 * quarter + lane;
+        float va[64], vg[64], vu[64];
 #pragma unroll
-        for (int c = 0; c < 64; c += 16) {
-          uint32_t va[16], vg[16], vu[16];
-          tc_ld_32x32b_x16(ta + c, va);
-          tc_ld_32x32b_x16(tg + c, vg);
-          tc_ld_32x32b_x16(tg + 128 + c, vu);
-          tc_wait_ld();
+        for (int c = 0; c < 64; ++c) va[c] = vg[c] = vu[c] = 0.f;
+        for (int k0 = 0; k0 < nkH && ok; k0 += kChunk, ++n) {
+          auto add = [&](uint32_t t, float (&v)[64]) {
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) {
+              if (64 * half + c >= u.n) continue;
+              uint32_t r[16];
+              tc_ld_32x32b_x16(t_lane + t + 64 * half + c, r);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[c + j] += __uint_as_float(r[j]);
+            }
+          };
+          wait_acc(n & 1u, n >> 1);
+          if (!ok) break;
+          add(128 * (n & 1u), va);
+          release_acc(n & 1u);
+          wait_acc(2, n);
+          if (!ok) break;
+          add(256, vg);
+          add(384, vu);
+          release_acc(2);
+        }
+        if (!ok) break;
+        float* mine = sums + ((unit & 1) * kEpiWarps + warp - 4) * 64;
+        // 16 tokens at a time; the registers move up, so that the code is there once
+#pragma unroll 1
+        for (int c = 0; c < 64 && 64 * half + c < u.n; c += 16) {
+          const int t0 = 64 * half + c;
+          const int row = u.row + t0;
+          const float wr = t0 + (lane & 15) < u.m ? __ldg(a.weight + row + (lane & 15)) : 0.f;
+          float share[16];
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
             float dg[2], du[2], act[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const float av = __uint_as_float(va[j + q]), g = __uint_as_float(vg[j + q]);
-              const float uv = __uint_as_float(vu[j + q]);
+              const float w = __shfl_sync(0xffffffffu, wr, j + q);
+              const bool in = t0 + j + q < u.m;  // rows behind the last one: zeros for kDw's sums
+              const float av = va[j + q], g = vg[j + q], uv = vu[j + q];
               const float s = __fdividef(1.f, 1.f + __expf(-g));
-              const float gs = g * s, aw = av * wr;
-              share = fmaf(av, gs * uv, share);
-              dg[q] = aw * uv * (s + gs * (1.f - s));
-              du[q] = aw * gs;
-              act[q] = wr * gs * uv;
+              const float gs = g * s, aw = av * w;
+              share[j + q] = av * (gs * uv);
+              dg[q] = in ? aw * uv * (s + gs * (1.f - s)) : 0.f;
+              du[q] = in ? aw * gs : 0.f;
+              act[q] = in ? w * gs * uv : 0.f;
             }
-            const int i = (c + j) / 2;
-            pg[i] = in ? pack_bf16x2(dg[0], dg[1]) : 0u;  // the sums over rows go on to 64
-            pu[i] = in ? pack_bf16x2(du[0], du[1]) : 0u;
-            pa[i] = in ? pack_bf16x2(act[0], act[1]) : 0u;
+            __nv_bfloat16* to = a.dgu + (size_t)(row + j) * a.I;
+            store_pair(to, a.I, i, lane, i < a.I, dg[0], dg[1]);
+            store_pair(to + (size_t)a.Rp * a.I, a.I, i, lane, i < a.I, du[0], du[1]);
+            store_pair(a.act + (size_t)(row + j) * a.I, a.I, i, lane, i < a.I, act[0], act[1]);
+          }
+          const float s = lane_sums16(share, lane);
+          if ((lane & 1) == 0) mine[c + column_of(lane)] = s;
+#pragma unroll
+          for (int j = 0; j < 48; ++j) {
+            va[j] = va[j + 16];
+            vg[j] = vg[j + 16];
+            vu[j] = vu[j + 16];
           }
         }
-        tc_fence_before();
-        mbar_arrive(acc_empty(n & 1u));
-        mbar_arrive(acc_empty(2));
-        const int c0 = u.n0 + 64 * half;
-        if (in) a.share[(size_t)(c0 / 64) * a.Rp + row] = share;
-        if (c0 < a.I) {
+        // the four warps of these columns
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sums_bar(half));
+        if (!mbar_wait_bounded(sums_bar(half), unit & 1u, abort_flag, kWaitNs)) {
+          fail();
+          ok = false;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int t = 16 * quarter + lane;
+        if (lane < 16 && 64 * half + t < u.m) {
+          const float* s = sums + ((unit & 1) * kEpiWarps + 4 * half) * 64 + t;
+          a.share[(size_t)(u.m0 / 128 + rank) * a.Rp + u.row + 64 * half + t] =
+              (s[0] + s[64]) + (s[128] + s[192]);
+        }
+      }
+    } else if constexpr (MODE == kDx) {
+      while (ok && walk.next(u)) {
+        wait_acc(n & 1u, n >> 1);
+        if (!ok) break;
+        const int h = u.m0 + 128 * rank + 32 * quarter + lane;
+        const uint32_t t0 = t_lane + 256 * (n & 1u);
+        for (int c = 16 * half; c < u.m; c += 32) {
+          uint32_t v[16];
+          tc_ld_32x32b_x16(t0 + c, v);
+          tc_wait_ld();
+          float* to = a.rows + (size_t)(u.row + c) * a.H + h;
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const uint32_t(&v)[32] = k == 0 ? pg : k == 1 ? pu : pa;
+          for (int j = 0; j < 16; ++j)
+            if (c + j < u.m && h < a.H) to[(size_t)j * a.H] = __uint_as_float(v[j]);
+        }
+        release_acc(n & 1u);
+        ++n;
+      }
+    } else {
+      uint8_t* boxes = epi + (warp - 4) * 2 * kBoxBytes;
+      uint32_t stores = 0;
+      constexpr int kCols = F32 ? 32 : 64;  // of a box
+      while (ok && walk.next(u)) {
+        const int r0 = u.m0 + 128 * rank + 32 * quarter;  // the warp's first row of the matrix
+        const bool in = r0 < (u.part == 2 ? a.H : a.I);
+        const CUtensorMap* map = u.part == 0 ? &maps.o0 : u.part == 1 ? &maps.o1 : &maps.o2;
+        const int c1 = in ? min(u.n, half * 128 + 128) : 0;
+        if (u.m == 0) {
+          // an expert without rows: zeros, or nothing to add
+          if (a.accumulate) continue;
+          for (int c = half * 128; c < c1; c += kCols) {
+            uint8_t* box = boxes + (stores++ & 1) * kBoxBytes;
+            box_wait(lane);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) box_piece(box, lane, i, make_uint4(0u, 0u, 0u, 0u));
+            box_store(map, box, lane, u.n0 + c, r0, u.e, false);
+          }
+          continue;
+        }
+        wait_acc(n & 1u, n >> 1);
+        if (!ok) break;
+        const uint32_t t0 = t_lane + 256 * (n & 1u) + 128 * half;
+        if constexpr (F32) {
+          for (int c = 128 * half; c < c1; c += kCols) {
+            uint32_t v[32];
+            tc_ld_32x32b_x32(t0 - 128 * half + c, v);
+            tc_wait_ld();
+            uint8_t* box = boxes + (stores++ & 1) * kBoxBytes;
             box_wait(lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               box_piece(box, lane, i, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-            box_store(k == 2 ? &maps.o1 : &maps.o0, box, lane, c0, u.row + r0, k == 1, false);
+            box_store(map, box, lane, u.n0 + c, r0, u.e, a.accumulate);
           }
-        }
-      } else {
-        constexpr bool kF = MODE == kDx || F32;  // 32 columns of a row per 128 bytes, or 64
-        const uint32_t t0 = t_lane + 256 * (n & 1u);
-        const int rows = MODE == kDx ? 128 : u.part == 2 ? a.H : a.I;
-        const CUtensorMap* map = u.part == 0 ? &maps.o0 : u.part == 1 ? &maps.o1 : &maps.o2;
-        const int c1 = min(u.n, half * 128 + 128);
-        if (u.m0 + r0 < rows) {
-          for (int c = half * 128; c < c1; c += kF ? 32 : 64) {
-            uint32_t v[kF ? 32 : 64];
+          release_acc(n & 1u);
+        } else {
+          // all of the warp's columns first, so that the accumulator is free before the stores
+          uint32_t o[64];
 #pragma unroll
-            for (int i = 0; i < (kF ? 32 : 64); i += 16)
-              tc_ld_32x32b_x16(t0 + c + i, *reinterpret_cast<uint32_t(*)[16]>(v + i));
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t v[32];
+            tc_ld_32x32b_x32(t0 + c, v);
             tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              o[c / 2 + j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+          }
+          release_acc(n & 1u);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (128 * half + 64 * c >= c1) continue;
+            uint8_t* box = boxes + (stores++ & 1) * kBoxBytes;
             box_wait(lane);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if constexpr (kF) {
-                box_piece(box, lane, i, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-              } else {
-                uint32_t o[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  o[q] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * q]), __uint_as_float(v[8 * i + 2 * q + 1]));
-                box_piece(box, lane, i, make_uint4(o[0], o[1], o[2], o[3]));
-              }
-            }
-            if constexpr (MODE == kDx) box_store(map, box, lane, u.n0 + c, u.row + r0, 0, false);
-            else box_store(map, box, lane, u.n0 + c, u.m0 + r0, u.e, a.accumulate);
+            for (int i = 0; i < 8; ++i)
+              box_piece(box, lane, i,
+                        make_uint4(o[32 * c + 4 * i], o[32 * c + 4 * i + 1], o[32 * c + 4 * i + 2],
+                                   o[32 * c + 4 * i + 3]));
+            box_store(map, box, lane, u.n0 + 128 * half + 64 * c, r0, u.e, false);
           }
         }
-        tc_fence_before();
-        mbar_arrive(acc_empty(n & 1u));
+        ++n;
       }
-      ++n;
+      if (lane == 0) bulk_wait();  // the stores are done before the CTA is
     }
-    if (lane == 0) bulk_wait();  // the stores are done before the CTA is
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may still reach it
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc2(tmem, 512);
 }
 
 // ---------------------------------------------------------------- finish
@@ -640,10 +866,10 @@ finish_kernel(const FinishArgs a) {
 template <int MODE, bool F32>
 cudaError_t run_products(const Maps& maps, const GradArgs& a, cudaStream_t stream) {
   static std::atomic<unsigned long long> set{0};
-  const cudaError_t e = moe_raise_smem(products_kernel<MODE, F32>, kSmemBytes, set);
+  const cudaError_t e = moe_raise_smem(products_kernel<MODE, F32>, Cfg<MODE>::kSmemBytes, set);
   if (e != cudaSuccess) return e;
-  return moe_launch(products_kernel<MODE, F32>, dim3(moe_num_sms()), dim3(kThreads), kSmemBytes, stream,
-                    1, maps, a);
+  return moe_launch_clusters(products_kernel<MODE, F32>, dim3(moe_num_sms() & ~1), dim3(kThreads),
+                             Cfg<MODE>::kSmemBytes, stream, dim3(2), maps, a);  // pairs lie along x
 }
 
 }  // namespace
@@ -662,25 +888,36 @@ cudaError_t launch_experts_backward(const ExpertsBackwardArgs& g, void* scratch,
   char* dp = xp + (size_t)l.Rp * H * 2;
   char* dgu = s + l.act;
   char* act = dgu + (size_t)l.Rp * I * 4;
-  GradArgs a{reinterpret_cast<const Plan*>(s), reinterpret_cast<const int2*>(s + l.tile),
-             reinterpret_cast<const float*>(s + l.weight), reinterpret_cast<float*>(s + l.share),
-             l.Rp, H, I, E, g.accumulate, g.dev_status};
+  GradArgs a{};
+  a.plan = reinterpret_cast<const Plan*>(s);
+  a.weight = reinterpret_cast<const float*>(s + l.weight);
+  a.share = reinterpret_cast<float*>(s + l.share);
+  a.dgu = reinterpret_cast<__nv_bfloat16*>(dgu);
+  a.act = reinterpret_cast<__nv_bfloat16*>(act);
+  a.rows = reinterpret_cast<float*>(xp);
+  a.Rp = l.Rp; a.H = H; a.I = I; a.E = E;
+  a.accumulate = g.accumulate;
+  a.dev_status = g.dev_status;
 
-  RowArgs r{static_cast<const uint4*>(g.x), static_cast<const uint4*>(g.dout),
-            static_cast<const uint4*>(g.xq), g.xq_scale, g.offsets, g.row_to_flat, g.weights, R, H, E, K,
-            reinterpret_cast<Plan*>(s), reinterpret_cast<int2*>(s + l.tile),
-            reinterpret_cast<int32_t*>(s + l.place), reinterpret_cast<float*>(s + l.weight),
-            reinterpret_cast<uint4*>(xp), reinterpret_cast<uint4*>(dp)};
+  RowArgs r{};
+  r.x = static_cast<const uint4*>(g.x); r.dout = static_cast<const uint4*>(g.dout);
+  r.xq = static_cast<const uint4*>(g.xq); r.xs = g.xq_scale;
+  r.offsets = g.offsets; r.row_to_flat = g.row_to_flat; r.weights = g.weights;
+  r.R = R; r.H = H; r.E = E; r.K = K;
+  r.plan = reinterpret_cast<Plan*>(s);
+  for (int i = 0; i < 2; ++i) a.tile[i] = r.tile[i] = reinterpret_cast<Tile*>(s + l.tile[i]);
+  r.place = reinterpret_cast<int32_t*>(s + l.place);
+  r.weight = reinterpret_cast<float*>(s + l.weight);
+  r.xp = reinterpret_cast<uint4*>(xp); r.dp = reinterpret_cast<uint4*>(dp);
   const int blocks = (int)(l.Rp / 4 < 152 * 8 ? l.Rp / 4 : 152 * 8);
   cudaError_t e = moe_launch(g.xq ? rows_kernel<true> : rows_kernel<false>, dim3(blocks), dim3(256), 0,
                              stream, 1, r);
   if (e != cudaSuccess) return e;
 
   Maps m{};
-  bool ok = bf16_map_3d(&m.a0, dp, H, l.Rp, 1, 64, 128) && bf16_map_3d(&m.a1, xp, H, l.Rp, 1, 64, 128) &&
-            bf16_map_3d(&m.b0, g.w1, H, I, E, 64, 128) && bf16_map_3d(&m.b1, g.w3, H, I, E, 64, 128) &&
-            bf16_map_3d(&m.b2, g.w2, I, H, E, 64, 64) && bf16_map_3d(&m.o0, dgu, I, l.Rp, 2, 64, 32) &&
-            bf16_map_3d(&m.o1, act, I, l.Rp, 1, 64, 32);
+  bool ok = bf16_map_3d(&m.a0, g.w1, H, I, E, 64, 128) && bf16_map_3d(&m.a1, g.w3, H, I, E, 64, 128) &&
+            bf16_map_3d(&m.a2, g.w2, I, H, E, 64, 64) && bf16_map_3d(&m.b0, xp, H, l.Rp, 1, 64, 64) &&
+            bf16_map_3d(&m.b1, dp, H, l.Rp, 1, 64, 64);
   if (!ok) return cudaErrorInvalidValue;
   if (R > 0 && (e = run_products<kAct, false>(m, a, stream)) != cudaSuccess) return e;
 
@@ -698,8 +935,8 @@ cudaError_t launch_experts_backward(const ExpertsBackwardArgs& g, void* scratch,
   }
   if (g.dx && R > 0) {
     m = Maps{};
-    ok = bf16_map_3d(&m.a0, dgu, I, l.Rp, 2, 64, 128) && bf16_map_3d(&m.b0, g.w1, H, I, E, 64, 64) &&
-         bf16_map_3d(&m.b1, g.w3, H, I, E, 64, 64) && f32_map_3d(&m.o0, xp, H, l.Rp, 1, 32, 32);
+    ok = bf16_map_3d(&m.a0, g.w1, H, I, E, 64, 64) && bf16_map_3d(&m.a1, g.w3, H, I, E, 64, 64) &&
+         bf16_map_3d(&m.b0, dgu, I, l.Rp, 2, 64, 64);
     if (!ok) return cudaErrorInvalidValue;
     if ((e = run_products<kDx, false>(m, a, stream)) != cudaSuccess) return e;
   }
