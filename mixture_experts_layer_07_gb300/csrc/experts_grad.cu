@@ -38,6 +38,7 @@
 
 #include "common.cuh"
 #include "e4m3.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 #include "sm100_ptx.cuh"
 #include "tmap.h"
@@ -45,6 +46,7 @@
 namespace {
 
 using namespace moe_e4m3;
+using namespace moe_f32x2;
 using namespace moe_ptx;
 
 constexpr uint64_t kWaitNs = 2000000000ull;  // every wait gives up after 2 s
@@ -231,8 +233,8 @@ struct Cfg {
   static constexpr int kStageBytes = MODE == kAct ? 2 * kTile + kTile / 2 : 2 * kTile;
   static constexpr int kB = MODE == kAct ? 2 * kTile : kTile;  // where B lies in a stage
   static constexpr int kStages = MODE == kDx ? 6 : 5;
-  // kDw: two boxes per warp; kAct: two sets of the warps' column sums
-  static constexpr int kEpiBytes = MODE == kDw ? 2 * kEpiWarps * kBoxBytes : kEpiWarps * 64 * 4 * 2;
+  // kDw: two boxes per warp; kAct: two sets of the warps' column sums, the tokens' weights
+  static constexpr int kEpiBytes = MODE == kDw ? 2 * kEpiWarps * kBoxBytes : kEpiWarps * 64 * 4 * 3;
   static constexpr int kNumBars = 2 * kStages + 3 + 3 + 1 + 2;
   static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kEpiBytes + kNumBars * 8 + 16;
   static_assert(kSmemBytes <= 232448, "227 KB of shared memory per CTA");
@@ -360,12 +362,19 @@ MOE_DEVICE int column_of(int lane) {
   return (lane >> 4 & 1) * 8 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2 + (lane >> 1 & 1);
 }
 
-// Two tokens' values of this lane's feature to two rows of bf16: even lanes store two
-// features of the first token, odd lanes two of the second.
-MOE_DEVICE void store_pair(__nv_bfloat16* row0, int pitch, int feature, int lane, bool in, float v0, float v1) {
-  const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
-  const uint32_t two = lane & 1 ? pack_bf16x2(got, v1) : pack_bf16x2(v0, got);
-  if (in) *reinterpret_cast<uint32_t*>(row0 + (size_t)(lane & 1) * pitch + (feature & ~1)) = two;
+// Two tokens' values of this lane's feature -> two features' of one token: even lanes get
+// the first token's, odd lanes the second's; `pick` is 0x5410 in even lanes, 0x3276 in odd.
+MOE_DEVICE uint32_t turn_pair(float2 v, uint32_t pick) {
+  const uint32_t mine = pack_bf16x2(v.x, v.y);
+  return __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), pick);
+}
+
+// 1 / (1 + e^-g) from the hardware's 2^x and 1 / x (2^-22 relative each)
+MOE_DEVICE float sigmoid(float g) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
 }
 
 // F32: the matrices' gradients in fp32 (kDw), else bf16
@@ -621,9 +630,15 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
     };
     if constexpr (MODE == kAct) {
       float* sums = reinterpret_cast<float*>(epi);  // [2][warps][64]
+      float* wts = sums + (2 * kEpiWarps + warp - 4) * 64;
       for (uint32_t unit = 0; ok && walk.next(u); ++unit) {
         // a thread's feature; its columns (tokens) 64 half .. + 63
         const int i = u.m0 + 128 * rank + 32 * quarter + lane;
+        // its tokens' weights, where the whole warp reads them
+        __syncwarp();
+        for (int t = lane; t < 64; t += 32)
+          wts[t] = 64 * half + t < u.m ? __ldg(a.weight + u.row + 64 * half + t) : 0.f;
+        __syncwarp();
         float va[64], vg[64], vu[64];
 #pragma unroll
         for (int c = 0; c < 64; ++c) va[c] = vg[c] = vu[c] = 0.f;
@@ -636,7 +651,12 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
               tc_ld_32x32b_x16(t_lane + t + 64 * half + c, r);
               tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[c + j] += __uint_as_float(r[j]);
+              for (int j = 0; j < 16; j += 2) {
+                const float2 x = add2(make_float2(v[c + j], v[c + j + 1]),
+                                      make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
+                v[c + j] = x.x;
+                v[c + j + 1] = x.y;
+              }
             }
           };
           wait_acc(n & 1u, n >> 1);
@@ -651,40 +671,55 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
         }
         if (!ok) break;
         float* mine = sums + ((unit & 1) * kEpiWarps + warp - 4) * 64;
-        // 16 tokens at a time; the registers move up, so that the code is there once
+        // 32 tokens at a time; the registers move up, so that the code is there once
+        const bool in = i < a.I;
+        const uint32_t pick = lane & 1 ? 0x3276u : 0x5410u;
+        const size_t pitch = (size_t)a.I;
+        __nv_bfloat16* to = a.dgu + (size_t)(u.row + 64 * half + (lane & 1)) * pitch + (i & ~1);
+        __nv_bfloat16* to_act = a.act + (to - a.dgu);
+        const size_t to_du = (size_t)a.Rp * pitch;
 #pragma unroll 1
-        for (int c = 0; c < 64 && 64 * half + c < u.n; c += 16) {
-          const int t0 = 64 * half + c;
-          const int row = u.row + t0;
-          const float wr = t0 + (lane & 15) < u.m ? __ldg(a.weight + row + (lane & 15)) : 0.f;
-          float share[16];
+        for (int c = 0; c < 64 && 64 * half + c < u.n; c += 32) {
+          if (64 * half + c + 32 > u.m) {  // rows behind the last one: zeros for kDw's sums
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            float dg[2], du[2], act[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const float w = __shfl_sync(0xffffffffu, wr, j + q);
-              const bool in = t0 + j + q < u.m;  // rows behind the last one: zeros for kDw's sums
-              const float av = va[j + q], g = vg[j + q], uv = vu[j + q];
-              const float s = __fdividef(1.f, 1.f + __expf(-g));
-              const float gs = g * s, aw = av * w;
-              share[j + q] = av * (gs * uv);
-              dg[q] = in ? aw * uv * (s + gs * (1.f - s)) : 0.f;
-              du[q] = in ? aw * gs : 0.f;
-              act[q] = in ? w * gs * uv : 0.f;
-            }
-            __nv_bfloat16* to = a.dgu + (size_t)(row + j) * a.I;
-            store_pair(to, a.I, i, lane, i < a.I, dg[0], dg[1]);
-            store_pair(to + (size_t)a.Rp * a.I, a.I, i, lane, i < a.I, du[0], du[1]);
-            store_pair(a.act + (size_t)(row + j) * a.I, a.I, i, lane, i < a.I, act[0], act[1]);
+            for (int j = 0; j < 32; ++j)
+              if (64 * half + c + j >= u.m) va[j] = vg[j] = vu[j] = 0.f;
           }
-          const float s = lane_sums16(share, lane);
-          if ((lane & 1) == 0) mine[c + column_of(lane)] = s;
 #pragma unroll
-          for (int j = 0; j < 48; ++j) {
-            va[j] = va[j + 16];
-            vg[j] = vg[j + 16];
-            vu[j] = vu[j + 16];
+          for (int h = 0; h < 32; h += 16) {
+            if (64 * half + c + h >= u.n) continue;
+            float share[16];
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const float2 w = *reinterpret_cast<const float2*>(wts + c + h + j);
+              const float2 av = make_float2(va[h + j], va[h + j + 1]);
+              const float2 g = make_float2(vg[h + j], vg[h + j + 1]);
+              const float2 uv = make_float2(vu[h + j], vu[h + j + 1]);
+              const float2 s = make_float2(sigmoid(g.x), sigmoid(g.y));
+              const float2 gs = mul2(g, s), aw = mul2(av, w), t = mul2(gs, uv);
+              const float2 sh = mul2(av, t);
+              share[j] = sh.x;
+              share[j + 1] = sh.y;
+              const float2 f = fma2(gs, fma2(s, pair(-1.f), pair(1.f)), s);  // s (1 + g (1 - s))
+              const uint32_t dg = turn_pair(mul2(mul2(aw, uv), f), pick);
+              const uint32_t du = turn_pair(mul2(aw, gs), pick);
+              const uint32_t act = turn_pair(mul2(w, t), pick);
+              if (in) {
+                *reinterpret_cast<uint32_t*>(to) = dg;
+                *reinterpret_cast<uint32_t*>(to + to_du) = du;
+                *reinterpret_cast<uint32_t*>(to_act) = act;
+              }
+              to += 2 * pitch;
+              to_act += 2 * pitch;
+            }
+            const float s = lane_sums16(share, lane);
+            if ((lane & 1) == 0) mine[c + h + column_of(lane)] = s;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            va[j] = va[j + 32];
+            vg[j] = vg[j + 32];
+            vu[j] = vu[j + 32];
           }
         }
         // the four warps of these columns

@@ -283,8 +283,10 @@ MOE_DEVICE uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   return a;
 }
+// arrive on a barrier of either CTA.  Releases at CTA scope: it orders TMEM reads (with
+// tc_fence_before), not memory -- at cluster scope it would wait for this thread's stores.
 MOE_DEVICE void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // load into this CTA's shared memory; the bytes count on `bar` in either CTA of the pair
 MOE_DEVICE void tma_load2_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
