@@ -214,8 +214,9 @@ MOE_DEVICE void weight4(const void* w, int vec, float2* f) {
 // fp32 partial row is written.  (T = 8192, H = 7168: rows loaded into registers
 // when their turn comes 88 us; ring of two stages, two vectors per thread 86;
 // four stages, one vector, LAG 78; running offsets 76.)
-// HQ: h lies as e4m3 codes with a scale per row and 16 vectors; a stage's slot of
-// h then holds a vector's eight codes and, behind them, its scale.
+// HQ: h lies as e4m3 codes with a scale per row and 16 vectors.  An even lane copies the
+// codes of its vector and of its neighbour's (a copy per lane took the load queue: T = 8192,
+// H = 7168 92 us); the scales stay in registers, loaded a group ahead.
 template <int VPT, int S, int MAXT, int BPS, bool LAG, bool W32, bool HQ>
 __global__ void __launch_bounds__(MAXT, BPS)
 rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const void* __restrict__ h,
@@ -248,9 +249,8 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const void* __restrict
         const size_t o = o_issue + tpr * j;
         moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 0, j)), dy + o, 16);
         if constexpr (HQ) {
-          const uint32_t to = moe_ptx::smem_u32(slot_of(st, 1, j));
-          moe_ptx::cp_async_8(to, static_cast<const uint2*>(h) + o);
-          moe_ptx::cp_async_4(to + 8, hscale + (size_t)t_issue * ((H8 + 15) >> 4) + ((lt + tpr * j) >> 4), 4);
+          if ((threadIdx.x & 1) == 0)
+            moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 1, j)), static_cast<const uint2*>(h) + o, 16);
         } else {
           moe_ptx::cp_async_16(moe_ptx::smem_u32(slot_of(st, 1, j)), static_cast<const uint4*>(h) + o, 16);
         }
@@ -261,16 +261,27 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const void* __restrict
     t_issue += rows;
     o_issue += hop;
   };
-  // h of vector j in stage st
+  // h of vector j in stage st; HQ: its codes (they lie in the even lane's slot), whose scale
+  // goes into the factor that h is multiplied with
   auto load_h = [&](int st, int j, float2* f) {
-    const uint4 v = *slot_of(st, 1, j);
+    if constexpr (HQ)
+      codes4(*(reinterpret_cast<const uint2*>(slot_of(st, 1, j) - (threadIdx.x & 1)) + (threadIdx.x & 1)), f);
+    else
+      unpack4(*slot_of(st, 1, j), f);
+  };
+  struct Scales {
+    float v[HQ ? VPT : 1];
+  };
+  auto row_scales = [&](uint32_t t) {
+    Scales r;
     if constexpr (HQ) {
-      codes4(make_uint2(v.x, v.y), f);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) f[q] = mul2(f[q], pair(__uint_as_float(v.z)));
-    } else {
-      unpack4(v, f);
+      for (int j = 0; j < VPT; ++j)
+        r.v[j] = t < (uint32_t)T && lt + tpr * j < H8
+                     ? __ldg(hscale + (size_t)t * ((H8 + 15) >> 4) + ((lt + tpr * j) >> 4))
+                     : 0.f;
     }
+    return r;
   };
   auto row_rstd = [&](uint32_t t) { return t < (uint32_t)T ? __ldg(rstd + t) : 0.f; };
   constexpr bool kKeepW = VPT == 1;  // the weight stays in registers where they suffice
@@ -283,7 +294,7 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const void* __restrict
 
   // dx of the next group to finish, whose rows lie in stage st and whose dot
   // products in red[slot]
-  auto finish = [&](int st, int slot, float s, float dot) {
+  auto finish = [&](int st, int slot, float s, float dot, const Scales& sc) {
     if (wpr > 1) {
       dot = lane_id() < wpr ? red[slot][rs * wpr + lane_id()] : 0.f;
 #pragma unroll
@@ -296,11 +307,12 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const void* __restrict
       float2 gf[4], hf[4], wf[4], ef[4], o[4];
       unpack4(*slot_of(st, 0, j), gf);
       load_h(st, j, hf);
+      const float2 hc = pair(HQ ? c1 * sc.v[HQ ? j : 0] : c1);
       unpack4(dh ? *slot_of(st, 2, j) : make_uint4(0u, 0u, 0u, 0u), ef);
       if constexpr (!kKeepW) weight4<W32>(w, lt + tpr * j, wf);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        o[q] = fma2(pair(s), fma2(hf[q], pair(c1), mul2(gf[q], kKeepW ? wk[q] : wf[q])), ef[q]);
+        o[q] = fma2(pair(s), fma2(hf[q], hc, mul2(gf[q], kKeepW ? wk[q] : wf[q])), ef[q]);
       dx[o_done + tpr * j] = make_uint4(pack_bf16x2(o[0].x, o[0].y), pack_bf16x2(o[1].x, o[1].y),
                                         pack_bf16x2(o[2].x, o[2].y), pack_bf16x2(o[3].x, o[3].y));
     }
@@ -312,11 +324,15 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const void* __restrict
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) issue(i);
   float s = row_rstd(t), s_prev = 0.f, dot_prev = 0.f;
+  Scales sc = row_scales(t), sc_prev = sc;
   int it = 0;
   for (int g = blockIdx.x; g < groups; ++it, g += step) {
+    if constexpr (HQ) __syncwarp();  // the neighbour is done with the stage that is filled next
     issue((it + kAhead) % S);
     const float s_next = row_rstd(t + rows);
+    const Scales sc_next = row_scales(t + rows);
     moe_ptx::cp_async_wait<kAhead>();
+    if constexpr (HQ) __syncwarp();  // the neighbour's copy too
     const int st = it % S;
     float2 dot2 = pair(0.f);
     if (t < (uint32_t)T) {
@@ -326,10 +342,11 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const void* __restrict
         float2 gf[4], hf[4], wf[4];
         unpack4(*slot_of(st, 0, j), gf);
         load_h(st, j, hf);
+        const float2 hs = pair(HQ ? s * sc.v[HQ ? j : 0] : s);
         if constexpr (!kKeepW) weight4<W32>(w, lt + tpr * j, wf);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float2 n = mul2(hf[q], pair(s));
+          const float2 n = mul2(hf[q], hs);
           dw[j][q] = fma2(gf[q], n, dw[j][q]);
           dot2 = fma2(mul2(gf[q], kKeepW ? wk[q] : wf[q]), n, dot2);
         }
@@ -339,15 +356,17 @@ rmsnorm_backward_kernel(const uint4* dy, const uint4* dh, const void* __restrict
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if (wpr > 1 && lane_id() == 0) red[it & 1][warp_id()] = dot;
-    if (LAG && it > 0) finish((it - 1) % S, (it - 1) & 1, s_prev, dot_prev);
+    if (LAG && it > 0) finish((it - 1) % S, (it - 1) & 1, s_prev, dot_prev, sc_prev);
     if (wpr > 1) __syncthreads();
-    if (!LAG) finish(st, it & 1, s, dot);
+    if (!LAG) finish(st, it & 1, s, dot, sc);
     s_prev = s;
     dot_prev = dot;
     s = s_next;
+    sc_prev = sc;
+    sc = sc_next;
     t += rows;
   }
-  if (LAG && it > 0) finish((it - 1) % S, (it - 1) & 1, s_prev, dot_prev);
+  if (LAG && it > 0) finish((it - 1) % S, (it - 1) & 1, s_prev, dot_prev, sc_prev);
 
   float4* p = reinterpret_cast<float4*>(part) + (size_t)blockIdx.x * H8 * 2;
   // one row per block: its sums are the block's; else they meet in the ring,

@@ -4,97 +4,137 @@
 //   pack:   s = max |v| / 448 over the group, code = e4m3(v / s)
 //   unpack: v = bf16(code * s)
 //
-// Both are bound by memory: 3 bytes a value and a scale per 128.  Pack gives a group
-// to half a warp, a 16-byte vector per lane, so the maximum is four shuffles; a
-// thread has several vectors in flight.
+// Both are bound by memory (3 bytes a value and a scale per 128) once the work per
+// value is small enough.  Pack gives a group to four lanes, four 16-byte vectors each:
+// the scale and its reciprocal are then made once per 32 values, the maximum takes two
+// shuffles (a group per half warp, a vector per lane: 157 instructions per vector,
+// T = 8191, H = 7168 40 us).  Unpack takes 8 codes a lane and time, so that a warp's
+// stores are whole lines.
 #include "common.cuh"
 #include "e4m3.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 
 namespace {
 
 using namespace moe_e4m3;
+using namespace moe_f32x2;
 
 constexpr int kThreads = 256;
-constexpr int kVec = 4;  // vectors per thread: a block's loads are all in flight at once
+constexpr int kVec = 4;  // vectors per thread: all its loads are in flight at once
 
-// Slots of a row: its vectors, up to whole groups of 16.
+// The largest magnitude of 8 bf16 per half, as bits (a NaN is above every number).
+MOE_DEVICE uint32_t amax_bf16x8(const uint4& v) {
+  const uint32_t m = 0x7fff7fffu;
+  return __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+}
+
+// codes8 of 8 bf16, two values at a time; r = RN(1 / sc), sc within 2^+-80.
+MOE_DEVICE uint2 codes_bf16x8(const uint4& v, float sc, float r) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = make_float2(bf16_lo(u[i]), bf16_hi(u[i]));
+    const float2 q0 = mul2(f, pair(r));
+    const float2 q = fma2(fma2(q0, pair(-sc), f), pair(r), q0);
+    c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+// Four lanes per group of 16 vectors; G groups in a row (the last may hold fewer vectors).
 __global__ void __launch_bounds__(kThreads)
-pack_q8_kernel(const uint4* __restrict__ x, long long T, int H8, uint2* __restrict__ q,
+pack_q8_kernel(const uint4* __restrict__ x, long long T, int H8, int G, uint2* __restrict__ q,
                float* __restrict__ scale) {
   pdl_wait();
   pdl_trigger();
-  const int W = (H8 + 15) & ~15;
-  const long long first = (long long)blockIdx.x * (kThreads * kVec);
-  const long long r0 = first / W;
-  const int c0 = (int)(first % W) + threadIdx.x;
+  const long long first = (long long)blockIdx.x * (kThreads / 4);
+  const uint32_t at = (uint32_t)(first % G) + (threadIdx.x >> 2);
+  const long long row = first / G + at / (uint32_t)G;
+  const int g = at % (uint32_t)G, c0 = g * 16 + (threadIdx.x & 3);
+  const bool in = row < T;
+  const size_t base = (size_t)row * H8 + c0;
   uint4 v[kVec];
+  uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) {
-    const int i = c0 + j * kThreads, c = i % W;
-    const long long r = r0 + i / W;
-    v[j] = r < T && c < H8 ? __ldg(x + r * H8 + c) : make_uint4(0u, 0u, 0u, 0u);
-  }
+  for (int j = 0; j < kVec; ++j)
+    v[j] = in && c0 + 4 * j < H8 ? __ldg(x + base + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) {
-    const int i = c0 + j * kThreads, c = i % W;
-    const long long r = r0 + i / W;
-    float f[8];
-    bf16x8_to_f32(v[j], f);
-    uint32_t m = amax8(f);
+  for (int j = 0; j < kVec; ++j) m = __vmaxu2(m, amax_bf16x8(v[j]));
+  m = max(m >> 16, m & 0xffffu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  if (!in) return;
+  const float sc = __fdiv_rn(__uint_as_float(m << 16), 448.f);
+  if ((threadIdx.x & 3) == 0) scale[row * G + g] = sc;
+  if (sc > 0x1p-80f && sc < 0x1p80f) {
+    const float r = __frcp_rn(sc);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float sc = __fdiv_rn(__uint_as_float(m), 448.f);
-    if (r >= T || c >= H8) continue;
-    q[r * H8 + c] = codes8(f, sc);
-    if ((c & 15) == 0) scale[r * (W >> 4) + (c >> 4)] = sc;
+    for (int j = 0; j < kVec; ++j)
+      if (c0 + 4 * j < H8) q[base + 4 * j] = codes_bf16x8(v[j], sc, r);
+  } else {  // zeros, and scales near the range's ends
+#pragma unroll 1
+    for (int j = 0; j < kVec; ++j) {
+      float f[8];
+      bf16x8_to_f32(v[j], f);
+      if (c0 + 4 * j < H8) q[base + 4 * j] = codes8(f, sc);
+    }
   }
 }
 
-// 16 codes per vector.
+// 8 codes per vector, W of them in a row; a block's vectors follow one another.
 __global__ void __launch_bounds__(kThreads)
-unpack_q8_kernel(const uint4* __restrict__ q, const float* __restrict__ scale, long long T, int W,
+unpack_q8_kernel(const uint2* __restrict__ q, const float* __restrict__ scale, long long T, int W,
                  uint4* __restrict__ x) {
   pdl_wait();
   pdl_trigger();
-  const int groups = (W + 7) >> 3;
+  const int groups = (W + 15) >> 4;
   const long long first = (long long)blockIdx.x * (kThreads * kVec);
   const long long r0 = first / W;
-  const int c0 = (int)(first % W) + threadIdx.x;
-  uint4 v[kVec];
+  const uint32_t c0 = (uint32_t)(first % W) + threadIdx.x;
+  q += first + threadIdx.x;
+  x += first + threadIdx.x;
+  const long long left = T * W - first - threadIdx.x;
+  uint2 v[kVec];
   float s[kVec];
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
-    const int i = c0 + j * kThreads;
-    const long long r = r0 + i / W;
-    if (r >= T) continue;
-    v[j] = __ldg(q + r * W + i % W);
-    s[j] = __ldg(scale + r * groups + ((i % W) >> 3));
+    if (j * kThreads >= left) continue;
+    const uint32_t c = c0 + j * kThreads;
+    v[j] = __ldg(q + j * kThreads);
+    s[j] = __ldg(scale + (r0 + c / (uint32_t)W) * groups + ((c % (uint32_t)W) >> 4));
   }
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
-    const int i = c0 + j * kThreads;
-    const long long r = r0 + i / W;
-    if (r < T) decode16(v[j], s[j], x + (r * W + i % W) * 2);
+    if (j * kThreads >= left) continue;
+    float2 f[4];
+    codes4(v[j], f);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = mul2(f[i], pair(s[j]));
+      o[i] = pack_bf16x2(f[i].x, f[i].y);
+    }
+    x[j * kThreads] = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
-unsigned blocks_of(long long slots) {
-  return (unsigned)((slots + kThreads * kVec - 1) / (kThreads * kVec));
-}
+unsigned blocks_of(long long n, int per) { return (unsigned)((n + per - 1) / per); }
 
 }  // namespace
 
 cudaError_t launch_pack_q8(const void* x, int T, int H, void* xq, float* scale, cudaStream_t stream) {
-  const int H8 = H / 8;
-  return moe_launch(pack_q8_kernel, dim3(blocks_of((long long)T * ((H8 + 15) & ~15))), dim3(kThreads), 0,
-                    stream, 1, static_cast<const uint4*>(x), (long long)T, H8, static_cast<uint2*>(xq),
-                    scale);
+  const int G = (H + 127) / 128;
+  return moe_launch(pack_q8_kernel, dim3(blocks_of((long long)T * G, kThreads / 4)), dim3(kThreads), 0,
+                    stream, 1, static_cast<const uint4*>(x), (long long)T, H / 8, G,
+                    static_cast<uint2*>(xq), scale);
 }
 
 cudaError_t launch_unpack_q8(const void* xq, const float* scale, int T, int H, void* x,
                              cudaStream_t stream) {
-  return moe_launch(unpack_q8_kernel, dim3(blocks_of((long long)T * (H / 16))), dim3(kThreads), 0, stream,
-                    1, static_cast<const uint4*>(xq), scale, (long long)T, H / 16,
+  const int W = H / 8;
+  return moe_launch(unpack_q8_kernel, dim3(blocks_of((long long)T * W, kThreads * kVec)),
+                    dim3(kThreads), 0, stream, 1, static_cast<const uint2*>(xq), scale, (long long)T, W,
                     static_cast<uint4*>(x));
 }
