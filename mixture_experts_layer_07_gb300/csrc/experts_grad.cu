@@ -414,6 +414,11 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
     *abort_flag = 0;
     fence_mbar_init();
   }
+  if (warp == 0 && elect_one()) {
+    for (const CUtensorMap* m : {&maps.a0, &maps.a1, &maps.b0}) prefetch_tmap(m);
+    if (MODE == kAct) prefetch_tmap(&maps.a2);
+    if (MODE != kDx) prefetch_tmap(&maps.b1);
+  }
   if (warp == 1) {
     tmem_alloc2(smem_u32(tmem_slot), 512);
     tmem_relinquish2();
