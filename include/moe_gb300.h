@@ -464,7 +464,7 @@ moe_status_t moe_experts_backward_scratch_bytes(int T, int H, int E, int K, int 
  *   weights   [T, K] fp32
  *   w1, w3    [E, I, H];  w2 [E, H, I] bf16
  *   dx_add    [T, H] bf16 or NULL (a gradient that reaches the tokens another
- *             way, such as through the router)
+ *             way, such as through a shared expert)
  *   dx        [T, H] bf16 output or NULL; may be dx_add, dout or x
  *   d_weights [T, K] fp32 output or NULL
  *   dw1, dw3, dw2  outputs of the matrices' shapes, all three or none; of
