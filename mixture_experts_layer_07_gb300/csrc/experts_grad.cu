@@ -15,9 +15,8 @@
 //           the experts' order, zeros up to a whole 16 rows (the MMA's K)
 //   part 0  per up to 128 rows and 256 columns of I: a, g, u; writes dg, du, w act (bf16)
 //           and each 128 columns' share of <a, act>
-//   part 2  per expert: its three matrices' gradients, K = its rows
-//   part 1  per up to 256 rows and 256 columns of H: dg W1 + du W3 in fp32, over x's and
-//           dout's rows
+//   part 1  per up to 256 rows and 256 columns of H: dg W1 + du W3 in fp32; and per expert
+//           its three matrices' gradients, K = its rows
 //   finish  per token: the K rows' sum, and the shares of <a, act> added in order
 // The products are one kernel: 256 x N tiles by pairs of CTAs (tcgen05, cta_group::2, one
 // CTA per SM, persistent), a ring of 64-deep stages filled by TMA, accumulators in TMEM.
@@ -69,7 +68,7 @@ using Tile = int4;
 // Where things lie in the scratch.
 struct Layout {
   long long Rp;  // padded rows: at most R + 15 per expert that has any
-  size_t tile[2], place, weight, share, rows, act, total;
+  size_t tile[2], place, weight, share, rows, act, dx, total;
   int shares;
 };
 Layout layout_of(long long R, int H, int E, int I) {
@@ -89,8 +88,9 @@ Layout layout_of(long long R, int H, int E, int I) {
   l.place = take((size_t)R * 4);
   l.weight = take((size_t)l.Rp * 4);
   l.share = take((size_t)l.shares * l.Rp * 4);
-  l.rows = take((size_t)l.Rp * H * 4);  // x's rows, dout's rows; then dx's in fp32
+  l.rows = take((size_t)l.Rp * H * 4);  // x's rows, dout's rows
   l.act = take((size_t)l.Rp * I * 6);   // dg, du, w act
+  l.dx = take((size_t)l.Rp * H * 4);    // dx's rows, fp32
   l.total = moe_align_up(off, 256);
   return l;
 }
@@ -218,23 +218,24 @@ rows_kernel(const RowArgs a) {
 }
 
 // ---------------------------------------------------------------- products
-enum { kAct = 0, kDx = 1, kDw = 2 };  // the launches' parts
+enum { kAct = 0, kBack = 1 };  // the launches' parts
+enum { kW1 = 0, kW3 = 1, kW2 = 2, kX = 3 };  // what a unit of kBack is the gradient of
 
 constexpr int kBM = 256, kBK = 64;       // a pair's tile rows; a stage's K
 constexpr int kTile = 128 * kBK * 2;     // a CTA's 128 rows (or columns) of an operand, 64 deep
 constexpr int kPanel = 64 * kBK * 2;     // MN-major: 64 of M or N
 constexpr int kChunk = 4;                // kAct: stages between two additions in registers
 constexpr int kEpiWarps = 8;             // two per TMEM lane quarter, splitting the columns
-constexpr int kBoxBytes = 32 * 128;      // kDw: an epilogue warp's store, 32 rows of 128 bytes
+constexpr int kBoxBytes = 32 * 128;      // kBack: an epilogue warp's store, 32 rows of 128 bytes
 
 template <int MODE>
 struct Cfg {
   // kAct: W1, W3 (or W2) and half of 128 tokens; else A and half of 256 columns
   static constexpr int kStageBytes = MODE == kAct ? 2 * kTile + kTile / 2 : 2 * kTile;
   static constexpr int kB = MODE == kAct ? 2 * kTile : kTile;  // where B lies in a stage
-  static constexpr int kStages = MODE == kDx ? 6 : 5;
-  // kDw: two boxes per warp; kAct: two sets of the warps' column sums, the tokens' weights
-  static constexpr int kEpiBytes = MODE == kDw ? 2 * kEpiWarps * kBoxBytes : kEpiWarps * 64 * 4 * 3;
+  static constexpr int kStages = MODE == kBack ? 6 : 5;
+  // kBack: a box per warp; kAct: two sets of the warps' column sums, the tokens' weights
+  static constexpr int kEpiBytes = MODE == kBack ? kEpiWarps * kBoxBytes : kEpiWarps * 64 * 4 * 3;
   static constexpr int kNumBars = 2 * kStages + 3 + 3 + 1 + 2;
   static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kEpiBytes + kNumBars * 8 + 16;
   static_assert(kSmemBytes <= 232448, "227 KB of shared memory per CTA");
@@ -247,25 +248,22 @@ struct GradArgs {
   const float* weight;
   float* share;
   __nv_bfloat16 *dgu, *act;  // kAct's outputs: [2][Rp][I], [Rp][I]
-  float* rows;               // kDx's: [Rp][H]
+  float* rows;               // kBack's: [Rp][H]
   long long Rp;
   int H, I, E;
-  int accumulate;
+  bool dx, dw, accumulate;   // what is wanted: the gradient of x, of the matrices
   int32_t* dev_status;
 };
-// A and B of the parts' products, and what kDw stores.
-//   kAct: W1, W3, W2 | x's and dout's rows
-//   kDx:  W1, W3     | dg and du
-//   kDw:  dg and du, dout's rows | x's rows, w act | dW1, dW3, dW2
+// The operands, and the matrices' gradients.
 struct Maps {
-  CUtensorMap a0, a1, a2, b0, b1, o0, o1, o2;
+  CUtensorMap w1, w3, w2, x, dout, dgu, act, d1, d3, d2;
 };
 
 // One unit of work of a pair: a tile of one expert.
 struct Unit {
-  int e, row, m;   // expert; kAct, kDx: the tile's first padded row and its tokens; kDw: the expert's
+  int e, row, m;   // expert; the tile's first padded row and its tokens, or (matrices) the expert's
   int m0, n0, n;   // the tile's first row and column, its columns (a multiple of 16)
-  int part;        // kDw: which matrix
+  int part;        // kBack: kW1, kW3, kW2 or kX
 };
 
 // The units w, w + step, ... of a pair; what a unit needs from memory is loaded while
@@ -273,24 +271,28 @@ struct Unit {
 template <int MODE>
 struct Walk {
   const GradArgs& a;
-  int w, step, total, blocks, up, wI, wH;
+  int w, step, total, tokens, wI, wH;  // tokens: units of kAct, or of the gradient of x
   int4 raw;
 
   MOE_DEVICE Walk(const GradArgs& g, int first, int by) : a(g), w(first), step(by) {
     wI = moe_cdiv(a.I, kBM), wH = moe_cdiv(a.H, kBM);
-    up = wI * wH;  // dW1, dW3 and dW2 have as many blocks
-    blocks = MODE == kAct ? wI : MODE == kDx ? wH : 3 * up;
-    total = (MODE == kDw ? a.E : __ldg(&a.plan->tiles[MODE == kDx])) * blocks;
+    if constexpr (MODE == kAct) {
+      total = tokens = __ldg(&a.plan->tiles[0]) * wI;
+    } else {
+      // the gradient of x first: its units are the long ones
+      tokens = a.dx ? __ldg(&a.plan->tiles[1]) * wH : 0;
+      total = tokens + (a.dw ? a.E * 3 * wI * wH : 0);
+    }
     load();
   }
   MOE_DEVICE void load() {
     if (w >= total) return;
-    const int i = (uint32_t)w / (uint32_t)blocks;
-    if constexpr (MODE == kDw) {
-      const int2 r = __ldg(&a.plan->rows[i]);
-      raw = make_int4(i, 0, r.x, r.y);
+    if (MODE == kAct || w < tokens) {
+      raw = __ldg(a.tile[MODE] + (uint32_t)w / (uint32_t)(MODE == kAct ? wI : wH));
     } else {
-      raw = __ldg(a.tile[MODE == kDx] + i);
+      const int e = (uint32_t)(w - tokens) / (uint32_t)(3 * wI * wH);
+      const int2 r = __ldg(&a.plan->rows[e]);
+      raw = make_int4(e, 0, r.x, r.y);
     }
   }
   MOE_DEVICE bool next(Unit& u) {
@@ -298,25 +300,26 @@ struct Walk {
     u.e = raw.x;
     u.row = raw.z;
     u.m = raw.w;
-    u.part = 0;
-    if constexpr (MODE == kDw) {
-      int r = w - u.e * blocks;
-      u.part = r / up;
-      r -= u.part * up;
-      const int wide = u.part == 2 ? wI : wH;
-      u.m0 = r / wide * kBM;
-      u.n0 = r % wide * 256;
-      u.n = min(256, (u.part == 2 ? a.I : a.H) - u.n0);
-    } else {
+    if (MODE == kAct || w < tokens) {
       // an expert's tiles of one block follow one another, so its weights are read once
-      constexpr int kMost = MODE == kAct ? kActTokens : kDxTokens;
-      const int tiles = moe_cdiv(u.m, kMost), r = w - raw.y * blocks;
+      const int tiles = moe_cdiv(u.m, MODE == kAct ? kActTokens : kDxTokens);
+      const int r = w - raw.y * (MODE == kAct ? wI : wH);
       const int t = r % tiles, n = (moe_cdiv(u.m, tiles) + 15) & ~15;
+      u.part = kX;
       u.m0 = r / tiles * kBM;
       u.n0 = 0;
       u.row += t * n;
       u.m = min(n, u.m - t * n);
       u.n = (u.m + 15) & ~15;
+    } else {
+      // dW1, dW3 [I, H] and dW2 [H, I] have as many blocks each
+      int r = w - tokens - u.e * 3 * wI * wH;
+      u.part = r / (wI * wH);
+      r -= u.part * wI * wH;
+      const int wide = u.part == kW2 ? wI : wH;
+      u.m0 = r / wide * kBM;
+      u.n0 = r % wide * 256;
+      u.n = min(256, (u.part == kW2 ? a.I : a.H) - u.n0);
     }
     w += step;
     load();
@@ -325,9 +328,9 @@ struct Walk {
 };
 
 // A warp's 32 rows x 128 bytes from registers to the tensor: lane's row, as eight
-// 16-byte pieces, through one of the warp's two boxes.
+// 16-byte pieces, through the warp's box.
 MOE_DEVICE void box_wait(int lane) {
-  if (lane == 0) bulk_wait_read<1>();  // the store before the last one has read its box
+  if (lane == 0) bulk_wait_read<0>();  // the last store has read the box
   __syncwarp();
 }
 MOE_DEVICE void box_piece(uint8_t* box, int lane, int i, const uint4& v) {
@@ -377,7 +380,7 @@ MOE_DEVICE float sigmoid(float g) {
   return s;
 }
 
-// F32: the matrices' gradients in fp32 (kDw), else bf16
+// F32: the matrices' gradients in fp32, else bf16
 template <int MODE, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
 products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
@@ -415,9 +418,9 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
     fence_mbar_init();
   }
   if (warp == 0 && elect_one()) {
-    for (const CUtensorMap* m : {&maps.a0, &maps.a1, &maps.b0}) prefetch_tmap(m);
-    if (MODE == kAct) prefetch_tmap(&maps.a2);
-    if (MODE != kDx) prefetch_tmap(&maps.b1);
+    for (const CUtensorMap* m : {&maps.w1, &maps.w3, &maps.x, &maps.dout}) prefetch_tmap(m);
+    for (const CUtensorMap* m : {MODE == kAct ? &maps.w2 : &maps.dgu, MODE == kAct ? &maps.w2 : &maps.act})
+      prefetch_tmap(m);
   }
   if (warp == 1) {
     tmem_alloc2(smem_u32(tmem_slot), 512);
@@ -472,34 +475,34 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
             const int k1 = min(nkH, k0 + kChunk);
             for (int k = k0; k < k1 && ok; ++k)  // a = dout W2: W2 [H, I] lies MN-major
               if (take(kTile + kTile / 2)) {
-                tma_load2_3d(st, &maps.a2, bar, m0, k * kBK, u.e);
-                tma_load2_3d(st + kPanel, &maps.a2, bar, m0 + 64, k * kBK, u.e);
-                tma_load2_3d(st + C::kB, &maps.b1, bar, k * kBK, row, 0);
+                tma_load2_3d(st, &maps.w2, bar, m0, k * kBK, u.e);
+                tma_load2_3d(st + kPanel, &maps.w2, bar, m0 + 64, k * kBK, u.e);
+                tma_load2_3d(st + C::kB, &maps.dout, bar, k * kBK, row, 0);
               }
             for (int k = k0; k < k1 && ok; ++k)  // g, u
               if (take(2 * kTile + kTile / 2)) {
-                tma_load2_3d(st, &maps.a0, bar, k * kBK, m0, u.e);
-                tma_load2_3d(st + kTile, &maps.a1, bar, k * kBK, m0, u.e);
-                tma_load2_3d(st + C::kB, &maps.b0, bar, k * kBK, row, 0);
+                tma_load2_3d(st, &maps.w1, bar, k * kBK, m0, u.e);
+                tma_load2_3d(st + kTile, &maps.w3, bar, k * kBK, m0, u.e);
+                tma_load2_3d(st + C::kB, &maps.x, bar, k * kBK, row, 0);
               }
           }
-        } else if constexpr (MODE == kDx) {
+        } else if (u.part == kX) {
           const int row = u.row + half * rank;
           const bool two = half > 64;
           for (int part = 0; part < 2; ++part)  // W1 and W3 [I, H]: MN-major
             for (int k = 0; k < nkI && ok; ++k)
               if (take(kTile + (two ? 2 : 1) * kPanel)) {
-                const CUtensorMap* w = part ? &maps.a1 : &maps.a0;
+                const CUtensorMap* w = part ? &maps.w3 : &maps.w1;
                 tma_load2_3d(st, w, bar, m0, k * kBK, u.e);
                 tma_load2_3d(st + kPanel, w, bar, m0 + 64, k * kBK, u.e);
-                tma_load2_3d(st + C::kB, &maps.b0, bar, k * kBK, row, part);
-                if (two) tma_load2_3d(st + C::kB + kPanel, &maps.b0, bar, k * kBK, row + 64, part);
+                tma_load2_3d(st + C::kB, &maps.dgu, bar, k * kBK, row, part);
+                if (two) tma_load2_3d(st + C::kB + kPanel, &maps.dgu, bar, k * kBK, row + 64, part);
               }
         } else {
-          const int n0 = u.n0 + half * rank, part = u.part == 2 ? 0 : u.part;
+          const int n0 = u.n0 + half * rank, part = u.part == kW3;
           const bool two = half > 64;
-          const CUtensorMap* ma = u.part == 2 ? &maps.a1 : &maps.a0;
-          const CUtensorMap* mb = u.part == 2 ? &maps.b1 : &maps.b0;
+          const CUtensorMap* ma = u.part == kW2 ? &maps.dout : &maps.dgu;
+          const CUtensorMap* mb = u.part == kW2 ? &maps.act : &maps.x;
           for (int r = u.row; r < u.row + u.m && ok; r += kBK)
             if (take(kTile + (two ? 2 : 1) * kPanel)) {
               tma_load2_3d(st, ma, bar, m0, r, part);
@@ -550,7 +553,7 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
       const uint64_t dk = sdesc_k128_sw128(0), dmn = sdesc_mn_sw128(0, kPanel);
       constexpr int kK = 32 >> 4, kMn = 2048 >> 4;
       while (ok && walk.next(u)) {
-        const uint32_t id = idesc_bf16_f32(kBM, u.n) | (MODE == kDw ? kIdescMnB : 0u);
+        const uint32_t id = idesc_bf16_f32(kBM, u.n);
         if constexpr (MODE == kAct) {
           for (int k0 = 0; k0 < nkH && ok; k0 += kChunk, ++n) {
             const int k1 = min(nkH, k0 + kChunk);
@@ -585,10 +588,13 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
             done(2);
           }
         } else {
-          // kDx: all of K; kDw: the expert's rows, the last stage's as far as they go
-          const int k16 = MODE == kDx ? 8 * nkI : (u.m + 15) / 16;
+          // x: all of I, twice; the matrices: the expert's rows, the last stage's as far as they go
+          const bool of_x = u.part == kX;
+          const int k16 = of_x ? 8 * nkI : (u.m + 15) / 16;
           if (k16 == 0) continue;
-          const uint32_t d = tmem + 256 * (n & 1u);
+          const uint32_t d = tmem + 256 * (n & 1u), idb = id | kIdescMnA | (of_x ? 0u : kIdescMnB);
+          const uint64_t db = of_x ? dk : dmn;
+          const int kb = of_x ? kK : kMn;
           free_acc(n & 1u, n >> 1);
           for (int k = 0; k < k16 && ok; k += 4) {
             const uint32_t A = filled(), B = A + (C::kB >> 4);
@@ -596,9 +602,7 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
             if (elect_one()) {
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                if (MODE == kDx || k + q < k16)
-                  tc_mma2_f16(d, dmn + A + q * kMn, MODE == kDw ? dmn + B + q * kMn : dk + B + q * kK,
-                              id | kIdescMnA, k > 0 || q > 0);
+                if (k + q < k16) tc_mma2_f16(d, dmn + A + q * kMn, db + B + q * kb, idb, k > 0 || q > 0);
             }
             used();
           }
@@ -685,7 +689,7 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
         const size_t to_du = (size_t)a.Rp * pitch;
 #pragma unroll 1
         for (int c = 0; c < 64 && 64 * half + c < u.n; c += 32) {
-          if (64 * half + c + 32 > u.m) {  // rows behind the last one: zeros for kDw's sums
+          if (64 * half + c + 32 > u.m) {  // rows behind the last one: zeros for the matrices' sums
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (64 * half + c + j >= u.m) va[j] = vg[j] = vu[j] = 0.f;
@@ -708,11 +712,13 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
               const float2 f = fma2(gs, fma2(s, pair(-1.f), pair(1.f)), s);  // s (1 + g (1 - s))
               const uint32_t dg = turn_pair(mul2(mul2(aw, uv), f), pick);
               const uint32_t du = turn_pair(mul2(aw, gs), pick);
-              const uint32_t act = turn_pair(mul2(w, t), pick);
               if (in) {
                 *reinterpret_cast<uint32_t*>(to) = dg;
                 *reinterpret_cast<uint32_t*>(to + to_du) = du;
-                *reinterpret_cast<uint32_t*>(to_act) = act;
+              }
+              if (a.dw) {
+                const uint32_t act = turn_pair(mul2(w, t), pick);
+                if (in) *reinterpret_cast<uint32_t*>(to_act) = act;
               }
               to += 2 * pitch;
               to_act += 2 * pitch;
@@ -743,38 +749,37 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
               (s[0] + s[64]) + (s[128] + s[192]);
         }
       }
-    } else if constexpr (MODE == kDx) {
-      while (ok && walk.next(u)) {
-        wait_acc(n & 1u, n >> 1);
-        if (!ok) break;
-        const int h = u.m0 + 128 * rank + 32 * quarter + lane;
-        const uint32_t t0 = t_lane + 256 * (n & 1u);
-        for (int c = 16 * half; c < u.m; c += 32) {
-          uint32_t v[16];
-          tc_ld_32x32b_x16(t0 + c, v);
-          tc_wait_ld();
-          float* to = a.rows + (size_t)(u.row + c) * a.H + h;
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < u.m && h < a.H) to[(size_t)j * a.H] = __uint_as_float(v[j]);
-        }
-        release_acc(n & 1u);
-        ++n;
-      }
     } else {
-      uint8_t* boxes = epi + (warp - 4) * 2 * kBoxBytes;
-      uint32_t stores = 0;
+      uint8_t* box = epi + (warp - 4) * kBoxBytes;
       constexpr int kCols = F32 ? 32 : 64;  // of a box
       while (ok && walk.next(u)) {
+        if (u.part == kX) {
+          wait_acc(n & 1u, n >> 1);
+          if (!ok) break;
+          const int h = u.m0 + 128 * rank + 32 * quarter + lane;
+          const uint32_t t0 = t_lane + 256 * (n & 1u);
+          for (int c = 16 * half; c < u.m; c += 32) {
+            uint32_t v[16];
+            tc_ld_32x32b_x16(t0 + c, v);
+            tc_wait_ld();
+            float* to = a.rows + (size_t)(u.row + c) * a.H + h;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < u.m && h < a.H) to[(size_t)j * a.H] = __uint_as_float(v[j]);
+          }
+          release_acc(n & 1u);
+          ++n;
+          continue;
+        }
         const int r0 = u.m0 + 128 * rank + 32 * quarter;  // the warp's first row of the matrix
-        const bool in = r0 < (u.part == 2 ? a.H : a.I);
-        const CUtensorMap* map = u.part == 0 ? &maps.o0 : u.part == 1 ? &maps.o1 : &maps.o2;
+        const bool in = r0 < (u.part == kW2 ? a.H : a.I);
+        const CUtensorMap* map = u.part == kW1 ? &maps.d1 : u.part == kW3 ? &maps.d3 : &maps.d2;
         const int c1 = in ? min(u.n, half * 128 + 128) : 0;
         if (u.m == 0) {
           // an expert without rows: zeros, or nothing to add
           if (a.accumulate) continue;
           for (int c = half * 128; c < c1; c += kCols) {
-            uint8_t* box = boxes + (stores++ & 1) * kBoxBytes;
+            
             box_wait(lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i) box_piece(box, lane, i, make_uint4(0u, 0u, 0u, 0u));
@@ -790,7 +795,7 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
             uint32_t v[32];
             tc_ld_32x32b_x32(t0 - 128 * half + c, v);
             tc_wait_ld();
-            uint8_t* box = boxes + (stores++ & 1) * kBoxBytes;
+            
             box_wait(lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -814,7 +819,7 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             if (128 * half + 64 * c >= c1) continue;
-            uint8_t* box = boxes + (stores++ & 1) * kBoxBytes;
+            
             box_wait(lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -934,8 +939,10 @@ cudaError_t launch_experts_backward(const ExpertsBackwardArgs& g, void* scratch,
   a.share = reinterpret_cast<float*>(s + l.share);
   a.dgu = reinterpret_cast<__nv_bfloat16*>(dgu);
   a.act = reinterpret_cast<__nv_bfloat16*>(act);
-  a.rows = reinterpret_cast<float*>(xp);
+  a.rows = reinterpret_cast<float*>(s + l.dx);
   a.Rp = l.Rp; a.H = H; a.I = I; a.E = E;
+  a.dx = g.dx != nullptr && R > 0;
+  a.dw = g.dw1 != nullptr;
   a.accumulate = g.accumulate;
   a.dev_status = g.dev_status;
 
@@ -955,33 +962,25 @@ cudaError_t launch_experts_backward(const ExpertsBackwardArgs& g, void* scratch,
   if (e != cudaSuccess) return e;
 
   Maps m{};
-  bool ok = bf16_map_3d(&m.a0, g.w1, H, I, E, 64, 128) && bf16_map_3d(&m.a1, g.w3, H, I, E, 64, 128) &&
-            bf16_map_3d(&m.a2, g.w2, I, H, E, 64, 64) && bf16_map_3d(&m.b0, xp, H, l.Rp, 1, 64, 64) &&
-            bf16_map_3d(&m.b1, dp, H, l.Rp, 1, 64, 64);
+  bool ok = bf16_map_3d(&m.w1, g.w1, H, I, E, 64, 128) && bf16_map_3d(&m.w3, g.w3, H, I, E, 64, 128) &&
+            bf16_map_3d(&m.w2, g.w2, I, H, E, 64, 64) && bf16_map_3d(&m.x, xp, H, l.Rp, 1, 64, 64) &&
+            bf16_map_3d(&m.dout, dp, H, l.Rp, 1, 64, 64);
   if (!ok) return cudaErrorInvalidValue;
   if (R > 0 && (e = run_products<kAct, false>(m, a, stream)) != cudaSuccess) return e;
 
-  if (g.dw1) {
-    m = Maps{};
-    ok = bf16_map_3d(&m.a0, dgu, I, l.Rp, 2, 64, 64) && bf16_map_3d(&m.a1, dp, H, l.Rp, 1, 64, 64) &&
-         bf16_map_3d(&m.b0, xp, H, l.Rp, 1, 64, 64) && bf16_map_3d(&m.b1, act, I, l.Rp, 1, 64, 64);
+  if (a.dx || a.dw) {
+    ok = bf16_map_3d(&m.w1, g.w1, H, I, E, 64, 64) && bf16_map_3d(&m.w3, g.w3, H, I, E, 64, 64) &&
+         bf16_map_3d(&m.dgu, dgu, I, l.Rp, 2, 64, 64) && bf16_map_3d(&m.act, act, I, l.Rp, 1, 64, 64);
     auto out = [&](CUtensorMap* map, void* p, int n0, int n1) {
       return g.dw_f32 ? f32_map_3d(map, p, n0, n1, E, 32, 32) : bf16_map_3d(map, p, n0, n1, E, 64, 32);
     };
-    ok = ok && out(&m.o0, g.dw1, H, I) && out(&m.o1, g.dw3, H, I) && out(&m.o2, g.dw2, I, H);
+    if (a.dw) ok = ok && out(&m.d1, g.dw1, H, I) && out(&m.d3, g.dw3, H, I) && out(&m.d2, g.dw2, I, H);
     if (!ok) return cudaErrorInvalidValue;
-    e = g.dw_f32 ? run_products<kDw, true>(m, a, stream) : run_products<kDw, false>(m, a, stream);
+    e = g.dw_f32 ? run_products<kBack, true>(m, a, stream) : run_products<kBack, false>(m, a, stream);
     if (e != cudaSuccess) return e;
   }
-  if (g.dx && R > 0) {
-    m = Maps{};
-    ok = bf16_map_3d(&m.a0, g.w1, H, I, E, 64, 64) && bf16_map_3d(&m.a1, g.w3, H, I, E, 64, 64) &&
-         bf16_map_3d(&m.b0, dgu, I, l.Rp, 2, 64, 64);
-    if (!ok) return cudaErrorInvalidValue;
-    if ((e = run_products<kDx, false>(m, a, stream)) != cudaSuccess) return e;
-  }
   if (R == 0 || (!g.dx && !g.d_weights)) return cudaSuccess;
-  FinishArgs f{reinterpret_cast<const float4*>(xp), a.share, r.place, g.flat_to_row, g.offsets,
+  FinishArgs f{reinterpret_cast<const float4*>(a.rows), a.share, r.place, g.flat_to_row, g.offsets,
                static_cast<const uint4*>(g.dx_add), static_cast<uint4*>(g.dx), g.d_weights, l.Rp, T, K, H,
                E, l.shares};
   const long long warps = (g.dx ? (long long)T * moe_cdiv(H / 8, 32) : 0) + (g.d_weights ? moe_cdiv(R, 32) : 0);
