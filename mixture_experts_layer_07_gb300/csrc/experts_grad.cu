@@ -804,28 +804,25 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
           }
           release_acc(n & 1u);
         } else {
-          // all of the warp's columns first, so that the accumulator is free before the stores
-          uint32_t o[64];
-#pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t v[32];
-            tc_ld_32x32b_x32(t0 + c, v);
-            tc_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              o[c / 2 + j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-          }
-          release_acc(n & 1u);
+          // the second half's columns are read while the store takes the first's
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
+            uint32_t o[32];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              uint32_t v[32];
+              tc_ld_32x32b_x32(t0 + 64 * c + 32 * b, v);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                o[16 * b + j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            }
+            if (c == 1) release_acc(n & 1u);
             if (128 * half + 64 * c >= c1) continue;
-            
             box_wait(lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              box_piece(box, lane, i,
-                        make_uint4(o[32 * c + 4 * i], o[32 * c + 4 * i + 1], o[32 * c + 4 * i + 2],
-                                   o[32 * c + 4 * i + 3]));
+              box_piece(box, lane, i, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
             box_store(map, box, lane, u.n0 + 128 * half + 64 * c, r0, u.e, false);
           }
         }
