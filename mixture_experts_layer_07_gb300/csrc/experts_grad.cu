@@ -100,13 +100,13 @@ struct RowArgs {
   const uint4 *x, *dout;
   const uint4* xq;       // e4m3 codes and their scales, in place of x
   const float* xs;
-  const int32_t *offsets, *row_to_flat;
+  const int32_t *offsets, *row_to_flat, *flat_to_row;
   const float* weights;
   int R, H, E, K;
   Plan* plan;
   Tile* tile[2];
-  int32_t* place;
-  float* weight;
+  int32_t* place;  // of a replica: its padded row, -1 where it was dropped
+  float* weight;   // of a padded row
   uint4 *xp, *dp;
 };
 
@@ -120,7 +120,13 @@ rows_kernel(const RowArgs a) {
   __shared__ int at[kMaxE + 1];     // in the padded order
   pdl_wait();
   pdl_trigger();
-  const int E = a.E;
+  // Jobs of a warp: half of a row's copies each, x's or dout's, then the padding rows.  A job's
+  // replica is loaded a job ahead, the first one beside the offsets.
+  const int E = a.E, R = a.R;
+  const int warps = gridDim.x * (blockDim.x / 32);
+  const int first_job = blockIdx.x * (blockDim.x / 32) + warp_id();
+  auto flat_of = [&](long long j) { return j < 2ll * R ? __ldg(a.row_to_flat + (j >> 1)) : -1; };
+  int flat_next = flat_of(first_job);
   for (int e = threadIdx.x; e <= E; e += blockDim.x) first[e] = __ldg(a.offsets + e);
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -176,28 +182,39 @@ rows_kernel(const RowArgs a) {
     }
   }
   __syncthreads();
-  // a warp takes half of a padded row's copies: x's or dout's
+  const int rows = first[E];
+  for (int f = blockIdx.x * blockDim.x + threadIdx.x; f < R; f += gridDim.x * blockDim.x) {
+    const int r = __ldg(a.flat_to_row + f);
+    if (r < 0 || r >= rows) a.place[f] = -1;
+  }
   const int H8 = a.H / 8, lane = lane_id();
-  const int warps = gridDim.x * (blockDim.x / 32);
-  const long long jobs = 2ll * at[E];
-  for (long long j = blockIdx.x * (blockDim.x / 32) + warp_id(); j < jobs; j += warps) {
-    const int p = (int)(j >> 1);
+  for (long long j = first_job; j < 2ll * R + 32 * E; j += warps) {
     const bool of_x = (j & 1) == 0;
-    int e = 0;  // the last expert that starts at or before p
-    for (int lo = 0, hi = E; lo < hi;) {
-      const int mid = (lo + hi) >> 1;
-      if (at[mid + 1] <= p) lo = mid + 1; else hi = mid;
-      e = lo;
+    const int r = (int)(j >> 1);
+    int flat = flat_next, p;
+    flat_next = flat_of(j + warps);
+    if (r < R) {
+      if (r >= rows) continue;
+      int e = 0;  // the last expert that starts at or before r
+      for (int lo = 0, hi = E; lo < hi; e = lo) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid + 1] <= r) lo = mid + 1; else hi = mid;
+      }
+      if (r < first[e]) continue;  // offsets that do not start at 0
+      p = at[e] + r - first[e];
+      if (flat >= R) flat = -1;
+      if (of_x && lane == 0) {
+        if (flat >= 0) a.place[flat] = p;
+        a.weight[p] = flat >= 0 ? __ldg(a.weights + flat) : 0.f;
+      }
+    } else {
+      // up to 15 rows behind an expert's last one
+      const int e = (r - R) >> 4;
+      p = at[e] + first[e + 1] - first[e] + ((r - R) & 15);
+      if (p >= at[e + 1]) continue;
+      flat = -1;
+      if (of_x && lane == 0) a.weight[p] = 0.f;
     }
-    const int i = p - at[e], n = first[e + 1] - first[e];
-    int flat = -1;
-    if (i < n) {
-      const int row = first[e] + i;
-      flat = __ldg(a.row_to_flat + row);
-      if (of_x && lane == 0) a.place[row] = p;
-      if (flat >= a.R) flat = -1;
-    }
-    if (of_x && lane == 0) a.weight[p] = flat >= 0 ? __ldg(a.weights + flat) : 0.f;
     uint4* to = (of_x ? a.xp : a.dp) + (size_t)p * H8;
     if (flat < 0) {
       for (int c = lane; c < H8; c += 32) to[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -843,20 +860,19 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
 struct FinishArgs {
   const float4* rows;  // [Rp][H]
   const float* share;  // [shares][Rp]
-  const int32_t *place, *flat_to_row, *offsets;
+  const int32_t* place;
   const uint4* add;
   uint4* dx;
   float* d_weights;
   long long Rp;
-  int T, K, H, E, shares;
+  int T, K, H, shares;
 };
 
-// The padded row of replica f: -1 where it was dropped.
+// The padded row of replica f: -1 where it was dropped (or where the maps contradict each
+// other and its place was never written).
 MOE_DEVICE int padded_row(const FinishArgs& a, long long f) {
-  const int r = __ldg(a.flat_to_row + f);
-  if (r < 0 || r >= a.T * a.K || r >= __ldg(a.offsets + a.E)) return -1;
-  const int p = __ldg(a.place + r);
-  return p >= 0 && p < a.Rp ? p : -1;  // offsets that start above 0 leave places unset
+  const int p = __ldg(a.place + f);
+  return p >= 0 && p < a.Rp ? p : -1;
 }
 
 // A warp takes 256 columns of a token; behind those, 32 replicas' weights.
@@ -946,7 +962,8 @@ cudaError_t launch_experts_backward(const ExpertsBackwardArgs& g, void* scratch,
   RowArgs r{};
   r.x = static_cast<const uint4*>(g.x); r.dout = static_cast<const uint4*>(g.dout);
   r.xq = static_cast<const uint4*>(g.xq); r.xs = g.xq_scale;
-  r.offsets = g.offsets; r.row_to_flat = g.row_to_flat; r.weights = g.weights;
+  r.offsets = g.offsets; r.row_to_flat = g.row_to_flat; r.flat_to_row = g.flat_to_row;
+  r.weights = g.weights;
   r.R = R; r.H = H; r.E = E; r.K = K;
   r.plan = reinterpret_cast<Plan*>(s);
   for (int i = 0; i < 2; ++i) a.tile[i] = r.tile[i] = reinterpret_cast<Tile*>(s + l.tile[i]);
@@ -977,9 +994,9 @@ cudaError_t launch_experts_backward(const ExpertsBackwardArgs& g, void* scratch,
     if (e != cudaSuccess) return e;
   }
   if (R == 0 || (!g.dx && !g.d_weights)) return cudaSuccess;
-  FinishArgs f{reinterpret_cast<const float4*>(a.rows), a.share, r.place, g.flat_to_row, g.offsets,
+  FinishArgs f{reinterpret_cast<const float4*>(a.rows), a.share, r.place,
                static_cast<const uint4*>(g.dx_add), static_cast<uint4*>(g.dx), g.d_weights, l.Rp, T, K, H,
-               E, l.shares};
+               l.shares};
   const long long warps = (g.dx ? (long long)T * moe_cdiv(H / 8, 32) : 0) + (g.d_weights ? moe_cdiv(R, 32) : 0);
   return moe_launch(finish_kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, 1, f);
 }
