@@ -414,8 +414,8 @@ moe_status_t moe_add_rmsnorm_backward(const void* dy, const void* dh, const void
  *   x     [T, H] bf16;  xq [T, H] e4m3;  xq_scale [T, ceil(H / 128)] fp32 (the
  *         last group of a row may be narrower)
  * A group that holds an infinity or a NaN does not survive: its scale is not
- * finite and unpack gives NaN for all of it (for an infinity, NaN or infinities);
- * other groups are not touched by it.  H % 16 == 0; x and xq 16-byte aligned;
+ * finite and unpack gives NaN for all of it; other groups are not touched by it.
+ * H % 16 == 0; x and xq 16-byte aligned;
  * outputs overlap no input.  T == 0 does nothing, whatever the pointers are.
  */
 moe_status_t moe_pack_q8(const void* x, int T, int H, void* xq, float* xq_scale,
@@ -477,8 +477,10 @@ moe_status_t moe_experts_backward_scratch_bytes(int T, int H, int E, int K, int 
  *   dev_status  MOE_DEV_WAIT_TIMEOUT where a pipeline wait gave up, or NULL
  * Not all of dx, d_weights and dw1 may be NULL.  With E = 1 and K = 1 (offsets
  * 0, T and both maps 0 .. T-1) it is the gradient of a shared expert, weights
- * its gate.  Outputs overlap nothing else.  Deterministic.  T == 0 writes zeros
- * to the matrices' gradients (nothing with accumulate).
+ * its gate.  Outputs overlap nothing else.  Deterministic.  What is not finite in
+ * a token's x, dout or weights stays in its own outputs and in the gradients of the
+ * experts that it went to.  T == 0 writes zeros to the matrices' gradients (nothing
+ * with accumulate).  The gradient of permute alone is moe_unpermute with weights 1.
  */
 moe_status_t moe_experts_backward(const void* x, const void* xq, const float* xq_scale,
                                   const void* dout, const int32_t* offsets,

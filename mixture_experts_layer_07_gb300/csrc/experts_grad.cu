@@ -20,19 +20,29 @@
 //   finish  per token: the K rows' sum, and the shares of <a, act> added in order
 // The products are one kernel: 256 x N tiles by pairs of CTAs (tcgen05, cta_group::2, one
 // CTA per SM, persistent), a ring of 64-deep stages filled by TMA, accumulators in TMEM.
-// In parts 0 and 1 the tile's 256 are weight rows (features) and N the tokens, so that an
-// expert with few rows takes a narrow tile.  Operands that the sums run across the rows of
-// (W2 in a; W1, W3 in dx; both in the matrices' gradients) are read MN-major, as they lie.
-// A pair, because each SM then loads half of B only: with single CTAs and 128 x 256 tiles
-// the loads' 64 bytes per clock and SM were the bound (61 of them in part 0; T = 4096,
-// H = I = 2880, E = 32, K = 4: part 0 773 us, part 1 460, part 2 934).
+// Part 0's tiles and those of dx have weight rows (features) as their 256 and tokens as N,
+// so that an expert with few rows takes a narrow tile.  Operands that the sums run across
+// the rows of (W2 in a; W1, W3 in dx; both in the matrices' gradients) are read MN-major,
+// as they lie.  A pair, because each SM then loads half of B only: with single CTAs and
+// 128 x 256 tiles the loads' 64 bytes per clock and SM were the bound (61 of them in part 0).
 //
 // Roundings: dg, du and w act to bf16 (the tensor cores' operands), the outputs once.
 // Everything else is fp32.  The tensor cores cut what falls off an fp32 sum, which
 // shortens it by about 10^-8 per K of 16; a, g and u, whose errors d_weights shows (its
 // fp32 is not behind a rounding to bf16), are therefore taken out of TMEM every 256 of K
-// and added in registers (d_weights at H = 2880: 9e-6 off in one go).  No atomics: sums
-// have an order that the sizes and the routing fix.
+// and added in registers: d_weights is 6.5e-7 off 64 bits whatever H is, 9e-6 at H = 2880
+// in one go.  No atomics: sums have an order that the sizes and the routing fix.
+//
+// Measured on one GB300 (copy rate 6797 GB/s, bf16 1947 TFLOP/s), per call in a graph of them:
+//   T = 4096, H = I = 2880, E = 32, K = 4, from codes  1850 us (2343 with single CTAs); the
+//     tensor cores' 1116 us, at the lower clock of long products, are the bound: part 0 is
+//     held by its loads (83 bytes per clock and SM at full rate) and by the 17 % of a unit
+//     that its epilogue does not hide, part 1 by loads and stores on the same path
+//   T = 2048, H = 2048, I = 768, E = 128, K = 8        716 us; memory: weights are read in
+//     part 0 and, but for W2, again in part 1 (6.1 and 6.0 TB/s under the profiler)
+//   T = 64, H = 2048, I = 512, E = 512, K = 10         1100 us, floor 948: the matrices'
+//     gradients, mostly zeros or one row's, have to be written
+//   T = 100, H = 256, I = 128, E = 8, K = 2            19 us: four dependent launches
 #include <cuda.h>
 
 #include "common.cuh"

@@ -7,9 +7,11 @@
 // Both are bound by memory (3 bytes a value and a scale per 128) once the work per
 // value is small enough.  Pack gives a group to four lanes, four 16-byte vectors each:
 // the scale and its reciprocal are then made once per 32 values, the maximum takes two
-// shuffles (a group per half warp, a vector per lane: 157 instructions per vector,
-// T = 8191, H = 7168 40 us).  Unpack takes 8 codes a lane and time, so that a warp's
-// stores are whole lines.
+// shuffles (a group per half warp, a vector per lane: 157 instructions per vector and
+// 40 us at T = 8191, H = 7168).  Unpack takes 8 codes a lane and time, so that a warp's
+// stores are whole lines (16 codes a lane: 20 us at T = 16384, H = 2048).
+// Measured on one GB300 (copy rate 6797 GB/s): pack T = 8191, H = 7168 33 us, 79 % of the
+// copy rate (2 us of it the launch); unpack T = 16384, H = 2048 16.6 us, 90 %; T = 1 1.5 us.
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "f32x2.cuh"

@@ -132,6 +132,19 @@ def test_many_wide_rows(ops, q8):
     Case(512, 2880, 4, 2, 2896, seed=3, skew=0.3, q8=q8).run(ops).check()
 
 
+def test_the_most_experts_and_replicas(ops):
+    c = Case(50, 32, 1024, 32, 48, seed=7).run(ops).check()
+    # and in a scratch that is aligned to no more than it has to be
+    n = ops.experts_backward_scratch_bytes(50, 32, 1024, 32, 48)
+    wide = torch.full((n + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+    want = c.outputs()
+    c.new_outputs()
+    start = (256 - wide.data_ptr()) % 512
+    assert (wide.data_ptr() + start) % 512 == 256
+    for a, b in zip(want, c.run(ops, wide[start:start + n]).outputs()):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("T,H,E,K,I", [(60, 128, 9, 2, 64), (1, 64, 3, 3, 32), (400, 144, 16, 4, 208)])
 def test_dropped_replicas(ops, T, H, E, K, I):
     c = Case(T, H, E, K, I, seed=5, drop=0.4).run(ops).check()
