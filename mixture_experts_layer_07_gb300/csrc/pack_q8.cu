@@ -5,13 +5,15 @@
 //   unpack: v = bf16(code * s)
 //
 // Both are bound by memory (3 bytes a value and a scale per 128) once the work per
-// value is small enough.  Pack gives a group to four lanes, four 16-byte vectors each:
-// the scale and its reciprocal are then made once per 32 values, the maximum takes two
-// shuffles (a group per half warp, a vector per lane: 157 instructions per vector and
-// 40 us at T = 8191, H = 7168).  Unpack takes 8 codes a lane and time, so that a warp's
-// stores are whole lines (16 codes a lane: 20 us at T = 16384, H = 2048).
-// Measured on one GB300 (copy rate 6797 GB/s): pack T = 8191, H = 7168 33 us, 79 % of the
-// copy rate (2 us of it the launch); unpack T = 16384, H = 2048 16.6 us, 90 %; T = 1 1.5 us.
+// value is small enough and enough loads are in flight.  Pack gives a group to four
+// lanes, four 16-byte vectors each: the scale and its reciprocal are then made once per
+// 32 values, the maximum takes two shuffles.  T = 8191, H = 7168: 40 us with a group per
+// half warp and a vector per lane (157 instructions per vector), 33 us with a group per
+// four lanes, 26.5 us with two of them (29 with three).  Unpack takes 8 codes a lane and
+// time, so that a warp's stores are whole lines (16 codes a lane: 20 us at T = 16384,
+// H = 2048, so 16.5).
+// Measured on one GB300 (copy rate 6797 GB/s): pack T = 8191, H = 7168 26.5 us, 99 % of
+// the copy rate; unpack T = 16384, H = 2048 16.5 us, 91 %; T = 1 1.4 us.
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "f32x2.cuh"
@@ -23,7 +25,9 @@ using namespace moe_e4m3;
 using namespace moe_f32x2;
 
 constexpr int kThreads = 256;
-constexpr int kVec = 4;  // vectors per thread: all its loads are in flight at once
+constexpr int kVec = 4;              // vectors of a group per lane (pack), vectors per thread (unpack)
+constexpr int kTeams = kThreads / 4;  // pack
+constexpr int kGroups = 2;            // pack: of a team
 
 // The largest magnitude of 8 bf16 per half, as bits (a NaN is above every number).
 MOE_DEVICE uint32_t amax_bf16x8(const uint4& v) {
@@ -46,41 +50,52 @@ MOE_DEVICE uint2 codes_bf16x8(const uint4& v, float sc, float r) {
 }
 
 // Four lanes per group of 16 vectors; G groups in a row (the last may hold fewer vectors).
+// A team takes two groups, a block's teams apart, all loads first.
 __global__ void __launch_bounds__(kThreads)
 pack_q8_kernel(const uint4* __restrict__ x, long long T, int H8, int G, uint2* __restrict__ q,
                float* __restrict__ scale) {
   pdl_wait();
   pdl_trigger();
-  const long long first = (long long)blockIdx.x * (kThreads / 4);
+  const long long first = (long long)blockIdx.x * (kTeams * kGroups);
+  const long long r0 = first / G;
   const uint32_t at = (uint32_t)(first % G) + (threadIdx.x >> 2);
-  const long long row = first / G + at / (uint32_t)G;
-  const int g = at % (uint32_t)G, c0 = g * 16 + (threadIdx.x & 3);
-  const bool in = row < T;
-  const size_t base = (size_t)row * H8 + c0;
-  uint4 v[kVec];
-  uint32_t m = 0;
+  uint4 v[kGroups][kVec];
 #pragma unroll
-  for (int j = 0; j < kVec; ++j)
-    v[j] = in && c0 + 4 * j < H8 ? __ldg(x + base + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-  for (int j = 0; j < kVec; ++j) m = __vmaxu2(m, amax_bf16x8(v[j]));
-  m = max(m >> 16, m & 0xffffu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  if (!in) return;
-  const float sc = __fdiv_rn(__uint_as_float(m << 16), 448.f);
-  if ((threadIdx.x & 3) == 0) scale[row * G + g] = sc;
-  if (sc > 0x1p-80f && sc < 0x1p80f) {
-    const float r = __frcp_rn(sc);
+  for (int b = 0; b < kGroups; ++b) {
+    const uint32_t a = at + b * kTeams;
+    const long long row = r0 + a / (uint32_t)G;
+    const int c0 = (int)(a % (uint32_t)G) * 16 + (threadIdx.x & 3);
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
-      if (c0 + 4 * j < H8) q[base + 4 * j] = codes_bf16x8(v[j], sc, r);
-  } else {  // zeros, and scales near the range's ends
-#pragma unroll 1
-    for (int j = 0; j < kVec; ++j) {
-      float f[8];
-      bf16x8_to_f32(v[j], f);
-      if (c0 + 4 * j < H8) q[base + 4 * j] = codes8(f, sc);
+      v[b][j] = row < T && c0 + 4 * j < H8 ? __ldg(x + (size_t)row * H8 + c0 + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int b = 0; b < kGroups; ++b) {
+    const uint32_t a = at + b * kTeams;
+    const long long row = r0 + a / (uint32_t)G;
+    const int g = (int)(a % (uint32_t)G), c0 = g * 16 + (threadIdx.x & 3);
+    const size_t base = (size_t)row * H8 + c0;
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) m = __vmaxu2(m, amax_bf16x8(v[b][j]));
+    m = max(m >> 16, m & 0xffffu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if (row >= T) continue;
+    const float sc = __fdiv_rn(__uint_as_float(m << 16), 448.f);
+    if ((threadIdx.x & 3) == 0) scale[row * G + g] = sc;
+    if (sc > 0x1p-80f && sc < 0x1p80f) {
+      const float r = __frcp_rn(sc);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (c0 + 4 * j < H8) q[base + 4 * j] = codes_bf16x8(v[b][j], sc, r);
+    } else {  // zeros, and scales near the range's ends
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        float f[8];
+        bf16x8_to_f32(v[b][j], f);
+        if (c0 + 4 * j < H8) q[base + 4 * j] = codes8(f, sc);
+      }
     }
   }
 }
@@ -128,7 +143,7 @@ unsigned blocks_of(long long n, int per) { return (unsigned)((n + per - 1) / per
 
 cudaError_t launch_pack_q8(const void* x, int T, int H, void* xq, float* scale, cudaStream_t stream) {
   const int G = (H + 127) / 128;
-  return moe_launch(pack_q8_kernel, dim3(blocks_of((long long)T * G, kThreads / 4)), dim3(kThreads), 0,
+  return moe_launch(pack_q8_kernel, dim3(blocks_of((long long)T * G, kTeams * kGroups)), dim3(kThreads), 0,
                     stream, 1, static_cast<const uint4*>(x), (long long)T, H / 8, G,
                     static_cast<uint2*>(xq), scale);
 }
