@@ -30,19 +30,19 @@
 // Everything else is fp32.  The tensor cores cut what falls off an fp32 sum, which
 // shortens it by about 10^-8 per K of 16; a, g and u, whose errors d_weights shows (its
 // fp32 is not behind a rounding to bf16), are therefore taken out of TMEM every 256 of K
-// and added in registers: d_weights is 6.5e-7 off 64 bits whatever H is, 9e-6 at H = 2880
-// in one go.  No atomics: sums have an order that the sizes and the routing fix.
+// (the first 512 of a long one) and added in registers: d_weights is 7e-7 to 9e-7 off 64
+// bits whatever H is, 9e-6 at H = 2880 in one go.  No atomics: sums have an order that the sizes and the routing fix.
 //
 // Measured on one GB300 (copy rate 6797 GB/s, bf16 1947 TFLOP/s), per call in a graph of them:
-//   T = 4096, H = I = 2880, E = 32, K = 4, from codes  1850 us (2343 with single CTAs); the
+//   T = 4096, H = I = 2880, E = 32, K = 4, from codes  1830 us (2343 with single CTAs); the
 //     tensor cores' 1116 us, at the lower clock of long products, are the bound: part 0 is
-//     held by its loads (83 bytes per clock and SM at full rate) and by the 17 % of a unit
-//     that its epilogue does not hide, part 1 by loads and stores on the same path
-//   T = 2048, H = 2048, I = 768, E = 128, K = 8        716 us; memory: weights are read in
+//     held by its loads (83 bytes per clock and SM at full rate) and by what of its epilogue
+//     the next unit's first products do not hide, part 1 by loads and stores on the same path
+//   T = 2048, H = 2048, I = 768, E = 128, K = 8        715 us; memory: weights are read in
 //     part 0 and, but for W2, again in part 1 (6.1 and 6.0 TB/s under the profiler)
 //   T = 64, H = 2048, I = 512, E = 512, K = 10         1100 us, floor 948: the matrices'
 //     gradients, mostly zeros or one row's, have to be written
-//   T = 100, H = 256, I = 128, E = 8, K = 2            19 us: four dependent launches
+//   T = 100, H = 256, I = 128, E = 8, K = 2            18 us: four dependent launches
 #include <cuda.h>
 
 #include "common.cuh"
@@ -64,11 +64,16 @@ constexpr int kMaxE = 1024;
 // Tokens of a tile, at most; a tile of the gradient of x is wider, as it has one
 // accumulator where part 0 has three.
 constexpr int kActTokens = 128, kDxTokens = 256;
+// Part 0's tiles are halved, to 64 or 32 tokens, while all of its units still run at once:
+// a unit then ends earlier, as its epilogue is by the token (T = 512, H = 1024, I = 512,
+// E = 16, K = 4: 52.1 -> 50.7 us).  At most so many tiles more in the list.
+constexpr int kMoreTiles = 512;
 
 // What `rows` writes for the later launches, at the start of the scratch.
 struct Plan {
-  int32_t tiles[2];  // of part 0 and of part 1
-  int32_t pad[62];
+  int32_t tiles[2];    // of part 0 and of part 1
+  int32_t act_tokens;  // of a tile of part 0, at most
+  int32_t pad[61];
   int2 rows[kMaxE];  // an expert's first row in the padded order (a multiple of 16), its rows
 };
 // The tiles of an expert follow one another; each names the expert, the first of its
@@ -93,7 +98,7 @@ Layout layout_of(long long R, int H, int E, int I) {
     off = moe_align_up(off + bytes, 1024);
     return o;
   };
-  l.tile[0] = take((size_t)(R / kActTokens + some + 1) * sizeof(Tile));
+  l.tile[0] = take((size_t)(R / kActTokens + some + 1 + kMoreTiles) * sizeof(Tile));
   l.tile[1] = take((size_t)(R / kDxTokens + some + 1) * sizeof(Tile));
   l.place = take((size_t)R * 4);
   l.weight = take((size_t)l.Rp * 4);
@@ -113,6 +118,7 @@ struct RowArgs {
   const int32_t *offsets, *row_to_flat, *flat_to_row;
   const float* weights;
   int R, H, E, K;
+  int at_once;  // part 0's tiles that run at once
   Plan* plan;
   Tile* tile[2];
   int32_t* place;  // of a replica: its padded row, -1 where it was dropped
@@ -153,42 +159,47 @@ rows_kernel(const RowArgs a) {
     if (lane_id() == 0) before = 0;
     for (int e = lo; e < hi; ++e) first[e] = max(first[e], before);
     __syncwarp();
-    // sums over the experts before: padded rows, tiles of either kind
-    int s[3] = {0, 0, 0};
-    for (int e = lo; e < min(hi, E); ++e) {
-      const int n = first[e + 1] - first[e];
-      s[0] += (n + 15) & ~15;
-      s[1] += moe_cdiv(n, kActTokens);
-      s[2] += moe_cdiv(n, kDxTokens);
-    }
+    // sums over the experts before: padded rows, tiles of part 1, of part 0 by their size
+    constexpr int kSums = 5;
+    auto counts = [](int n, int (&c)[kSums]) {
+      c[0] += (n + 15) & ~15;
+      c[1] += moe_cdiv(n, kDxTokens);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+      for (int i = 2; i < kSums; ++i) c[i] += moe_cdiv(n, kActTokens >> (i - 2));
+    };
+    int s[kSums] = {0, 0, 0, 0, 0}, all[kSums];
+    for (int e = lo; e < min(hi, E); ++e) counts(first[e + 1] - first[e], s);
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) {
       int sum = s[i];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane_id() >= o) sum += v;
       }
+      all[i] = __shfl_sync(0xffffffffu, sum, 31);
       s[i] = sum - s[i];
     }
+    const int most = min(a.at_once, kMoreTiles);
+    const int half = all[4] <= most ? 2 : all[3] <= most ? 1 : 0;  // how often the tiles are halved
     for (int e = lo; e < hi; ++e) {
       at[e] = s[0];
       if (e == E) {
         if (blockIdx.x == 0) {
-          a.plan->tiles[0] = s[1];
-          a.plan->tiles[1] = s[2];
+          a.plan->tiles[0] = half == 2 ? all[4] : half == 1 ? all[3] : all[2];
+          a.plan->tiles[1] = all[1];
+          a.plan->act_tokens = kActTokens >> half;
         }
         break;
       }
       const int n = first[e + 1] - first[e];
       if (blockIdx.x == 0) {
+        const int t0 = half == 2 ? s[4] : half == 1 ? s[3] : s[2];
         a.plan->rows[e] = make_int2(s[0], n);
-        for (int j = 0; j < moe_cdiv(n, kActTokens); ++j) a.tile[0][s[1] + j] = make_int4(e, s[1], s[0], n);
-        for (int j = 0; j < moe_cdiv(n, kDxTokens); ++j) a.tile[1][s[2] + j] = make_int4(e, s[2], s[0], n);
+        for (int j = 0; j < moe_cdiv(n, kActTokens >> half); ++j) a.tile[0][t0 + j] = make_int4(e, t0, s[0], n);
+        for (int j = 0; j < moe_cdiv(n, kDxTokens); ++j) a.tile[1][s[1] + j] = make_int4(e, s[1], s[0], n);
       }
-      s[0] += (n + 15) & ~15;
-      s[1] += moe_cdiv(n, kActTokens);
-      s[2] += moe_cdiv(n, kDxTokens);
+      counts(n, s);
     }
   }
   __syncthreads();
@@ -252,6 +263,10 @@ constexpr int kBM = 256, kBK = 64;       // a pair's tile rows; a stage's K
 constexpr int kTile = 128 * kBK * 2;     // a CTA's 128 rows (or columns) of an operand, 64 deep
 constexpr int kPanel = 64 * kBK * 2;     // MN-major: 64 of M or N
 constexpr int kChunk = 4;                // kAct: stages between two additions in registers
+// and before a unit's first one: as many again where K is long (T = 4096, H = 2880 1893 ->
+// 1863 us, as the products run further ahead of the last unit's epilogue), which adds a
+// third to the sums' error at H = 1536, less above; below it would be more
+MOE_DEVICE int first_chunk(int stages) { return stages >= 24 ? 2 * kChunk : kChunk; }
 constexpr int kEpiWarps = 8;             // two per TMEM lane quarter, splitting the columns
 constexpr int kBoxBytes = 32 * 128;      // kBack: an epilogue warp's store, 32 rows of 128 bytes
 
@@ -299,13 +314,16 @@ template <int MODE>
 struct Walk {
   const GradArgs& a;
   int w, step, total, tokens, wI, wH;  // tokens: units of kAct, or of the gradient of x
+  int most;                            // tokens of a tile, at most
   int4 raw;
 
   MOE_DEVICE Walk(const GradArgs& g, int first, int by) : a(g), w(first), step(by) {
     wI = moe_cdiv(a.I, kBM), wH = moe_cdiv(a.H, kBM);
     if constexpr (MODE == kAct) {
+      most = __ldg(&a.plan->act_tokens);
       total = tokens = __ldg(&a.plan->tiles[0]) * wI;
     } else {
+      most = kDxTokens;
       // the gradient of x first: its units are the long ones
       tokens = a.dx ? __ldg(&a.plan->tiles[1]) * wH : 0;
       total = tokens + (a.dw ? a.E * 3 * wI * wH : 0);
@@ -329,7 +347,7 @@ struct Walk {
     u.m = raw.w;
     if (MODE == kAct || w < tokens) {
       // an expert's tiles of one block follow one another, so its weights are read once
-      const int tiles = moe_cdiv(u.m, MODE == kAct ? kActTokens : kDxTokens);
+      const int tiles = moe_cdiv(u.m, most);
       const int r = w - raw.y * (MODE == kAct ? wI : wH);
       const int t = r % tiles, n = (moe_cdiv(u.m, tiles) + 15) & ~15;
       u.part = kX;
@@ -498,8 +516,8 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
         const int m0 = u.m0 + 128 * rank, half = u.n / 2;
         if constexpr (MODE == kAct) {
           const int row = u.row + half * rank;
-          for (int k0 = 0; k0 < nkH && ok; k0 += kChunk) {
-            const int k1 = min(nkH, k0 + kChunk);
+          for (int k0 = 0, k1; k0 < nkH && ok; k0 = k1) {
+            k1 = min(nkH, k0 ? k0 + kChunk : first_chunk(nkH));
             for (int k = k0; k < k1 && ok; ++k)  // a = dout W2: W2 [H, I] lies MN-major
               if (take(kTile + kTile / 2)) {
                 tma_load2_3d(st, &maps.w2, bar, m0, k * kBK, u.e);
@@ -582,8 +600,8 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
       while (ok && walk.next(u)) {
         const uint32_t id = idesc_bf16_f32(kBM, u.n);
         if constexpr (MODE == kAct) {
-          for (int k0 = 0; k0 < nkH && ok; k0 += kChunk, ++n) {
-            const int k1 = min(nkH, k0 + kChunk);
+          for (int k0 = 0, k1; k0 < nkH && ok; k0 = k1, ++n) {
+            k1 = min(nkH, k0 ? k0 + kChunk : first_chunk(nkH));
             free_acc(n & 1u, n >> 1);
             for (int k = k0; k < k1 && ok; ++k) {
               const uint32_t A = filled(), d = tmem + 128 * (n & 1u);
@@ -681,7 +699,7 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
         float va[64], vg[64], vu[64];
 #pragma unroll
         for (int c = 0; c < 64; ++c) va[c] = vg[c] = vu[c] = 0.f;
-        for (int k0 = 0; k0 < nkH && ok; k0 += kChunk, ++n) {
+        for (int k0 = 0; k0 < nkH && ok; k0 = k0 ? k0 + kChunk : first_chunk(nkH), ++n) {
           auto add = [&](uint32_t t, float (&v)[64]) {
 #pragma unroll
             for (int c = 0; c < 64; c += 16) {
@@ -978,6 +996,7 @@ cudaError_t launch_experts_backward(const ExpertsBackwardArgs& g, void* scratch,
   r.offsets = g.offsets; r.row_to_flat = g.row_to_flat; r.flat_to_row = g.flat_to_row;
   r.weights = g.weights;
   r.R = R; r.H = H; r.E = E; r.K = K;
+  r.at_once = moe_num_sms() / 2 / moe_cdiv(I, kBM);
   r.plan = reinterpret_cast<Plan*>(s);
   for (int i = 0; i < 2; ++i) a.tile[i] = r.tile[i] = reinterpret_cast<Tile*>(s + l.tile[i]);
   r.place = reinterpret_cast<int32_t*>(s + l.place);
