@@ -352,3 +352,20 @@ def test_rows_past_32_bits(ops):
                      (d2[7], de.t() @ (wt * gate * s * up))):
         rel = float((got.to(D) - ref).norm() / ref.norm())
         assert rel < 2 * B, rel
+
+
+def test_two_calls_at_once(ops):
+    # on two streams, with a scratch each
+    cases = [Case(500, 512, 9, 3, 320, seed=s) for s in (1, 2)]
+    want = [c.run(ops).outputs() for c in cases]
+    scratch = [c.scratch(ops) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, w, s in zip(cases, scratch, streams):
+            c.run(ops, w, stream=s)
+    torch.cuda.synchronize()
+    for c, expected in zip(cases, want):
+        assert int(c.status) == 0
+        for a, b in zip(expected, c.outputs()):
+            assert torch.equal(a, b)
