@@ -38,9 +38,9 @@
 //     tensor cores' 1116 us, at the lower clock of long products, are the bound: part 0 is
 //     held by its loads (83 bytes per clock and SM at full rate) and by what of its epilogue
 //     the next unit's first products do not hide, part 1 by loads and stores on the same path
-//   T = 2048, H = 2048, I = 768, E = 128, K = 8        715 us; memory: weights are read in
+//   T = 2048, H = 2048, I = 768, E = 128, K = 8        711 us; memory: weights are read in
 //     part 0 and, but for W2, again in part 1 (6.1 and 6.0 TB/s under the profiler)
-//   T = 64, H = 2048, I = 512, E = 512, K = 10         1100 us, floor 948: the matrices'
+//   T = 64, H = 2048, I = 512, E = 512, K = 10         1081 us, floor 948: the matrices'
 //     gradients, mostly zeros or one row's, have to be written
 //   T = 100, H = 256, I = 128, E = 8, K = 2            18 us: four dependent launches
 #include <cuda.h>
@@ -373,7 +373,9 @@ struct Walk {
 };
 
 // A warp's 32 rows x 128 bytes from registers to the tensor: lane's row, as eight
-// 16-byte pieces, through the warp's box.
+// 16-byte pieces, through the warp's box.  The matrices' gradients are not read again
+// here: L2 gives their lines up first, which keeps dx's rows for `finish` (T = 64, E = 512
+// 1103 -> 1081 us, T = 2048, E = 128 714 -> 710).
 MOE_DEVICE void box_wait(int lane) {
   if (lane == 0) bulk_wait_read<0>();  // the last store has read the box
   __syncwarp();
@@ -387,7 +389,7 @@ MOE_DEVICE void box_store(const CUtensorMap* map, const uint8_t* box, int lane, 
   __syncwarp();
   if (lane == 0) {
     if (add) tma_reduce_add_3d(map, smem_u32(box), c0, c1, c2);
-    else tma_store_3d(map, smem_u32(box), c0, c1, c2);
+    else tma_store_3d_hint(map, smem_u32(box), c0, c1, c2, l2_evict_first());
     bulk_commit();
   }
 }

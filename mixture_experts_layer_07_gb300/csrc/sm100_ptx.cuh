@@ -120,6 +120,19 @@ MOE_DEVICE void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c
       "r"(src), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
+// the same for what is not read again soon: lines that L2 gives up first
+MOE_DEVICE uint64_t l2_evict_first() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+MOE_DEVICE void tma_store_3d_hint(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
 // the same, adding to what the tensor holds (in the tensor's type)
 MOE_DEVICE void tma_reduce_add_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
   asm volatile(
