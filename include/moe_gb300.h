@@ -436,7 +436,7 @@ moe_status_t moe_add_rmsnorm_backward_q8(const void* dy, const void* dh, const v
                                          void* dx, float* dweight, void* scratch,
                                          size_t scratch_bytes, moe_stream_t stream);
 
-/* Scratch bytes moe_experts_backward needs. */
+/* Scratch bytes moe_experts_backward needs: 8 H + 6 I per replica and some more. */
 moe_status_t moe_experts_backward_scratch_bytes(int T, int H, int E, int K, int I, size_t* bytes);
 
 /*

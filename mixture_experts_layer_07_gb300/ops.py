@@ -471,6 +471,21 @@ class MoELayer:
         layer(self.cfg, x, self.weights, out, self.workspace, self.dev_status, stream)
         return out
 
+    def experts_backward(self, dout, scratch, **kw):
+        """Gradients of the routed experts of the last call, from its routing as the workspace
+        holds it (bf16 experts): the tokens (x, or xq and xq_scale) and the outputs as
+        ops.experts_backward takes them.  A shared expert's gradient is a call of its own
+        (E = 1, weights its gate), which dx_add joins to this one."""
+        c, T, i32 = self.cfg, dout.shape[0], torch.int32
+        if T > c.T_max:
+            raise ValueError(f"dout: {T} tokens, the layer takes up to {c.T_max}")
+        w = self.tensors
+        experts_backward(dout, self.view("offsets", i32, (c.E + 1,)),
+                         self.view("row_to_flat", i32, (T * c.K,)),
+                         self.view("flat_to_row", i32, (T * c.K,)),
+                         self.view("weights", torch.float32, (T, c.K)), w["w1"], w["w3"], w["w2"],
+                         scratch, **{"dev_status": self.dev_status, **kw})
+
     def view(self, name, dtype, shape):
         """A typed view of one intermediate inside the workspace."""
         off = getattr(self.layout, name)

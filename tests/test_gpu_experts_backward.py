@@ -310,7 +310,16 @@ def test_routing_of_a_layer_as_it_left_it(ops, T):
     c.off, c.weights = view("offsets", I32, spec.E + 1), view("weights", F32, T, spec.K)
     c.r2f, c.f2r = view("row_to_flat", I32, T * spec.K), view("flat_to_row", I32, T * spec.K)
     c.ids = view("ids", I32, T, spec.K).cpu().numpy().astype(np.int64)
-    c.run(ops).check()
+    want = c.run(ops).check().outputs()
+    # and through the layer itself
+    c.new_outputs()
+    layer.experts_backward(c.dout, c.scratch(ops), x=c.x, dx_add=c.dx_add, dx=c.dx, d_weights=c.d_weights, dw1=c.dw1,
+                           dw3=c.dw3, dw2=c.dw2)
+    assert int(layer.dev_status) == 0
+    for a, b in zip(want, c.outputs()):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError, match="^dout: 257 tokens"):
+        layer.experts_backward(torch.empty(257, spec.H, dtype=BF16, device="cuda"), c.scratch(ops), x=c.x, dx=c.dx)
 
 
 def test_rows_past_32_bits(ops):
