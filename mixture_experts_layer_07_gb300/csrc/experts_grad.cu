@@ -245,8 +245,23 @@ rows_kernel(const RowArgs a) {
     if (Q && of_x) {
       const uint4* from = a.xq + t * (H8 / 2);
       const float* sc = a.xs + t * moe_cdiv(a.H, 128);
-#pragma unroll 4
-      for (int c = lane; c < H8 / 2; c += 32) decode16(__ldg(from + c), __ldg(sc + (c >> 3)), to + 2 * c);
+      // four pieces' loads before the first is decoded (T = 1023, K = 4, H = 2880 20.5 -> 18.8 us)
+      for (int c0 = 0; c0 < H8 / 2; c0 += 128) {
+        uint4 q[4];
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = c0 + 32 * i + lane;
+          if (c >= H8 / 2) continue;
+          q[i] = __ldg(from + c);
+          f[i] = __ldg(sc + (c >> 3));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = c0 + 32 * i + lane;
+          if (c < H8 / 2) decode16(q[i], f[i], to + 2 * c);
+        }
+      }
     } else {
       const uint4* from = (of_x ? a.x : a.dout) + t * H8;
 #pragma unroll 8
