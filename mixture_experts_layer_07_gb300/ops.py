@@ -451,7 +451,11 @@ class MoELayer:
     layer and calls ``moe_layer``.  Tensors are kept referenced so their
     pointers stay valid.  The workspace serves one call at a time: calls on
     different streams have to be ordered by the caller.  An output that a call
-    allocates belongs to the stream that the call runs on."""
+    allocates belongs to the stream that the call runs on.
+
+    ``tokens`` is the number of tokens of the last call, whose routing the
+    workspace holds (None before the first).  A replayed graph and a call of
+    ops.layer on this workspace go past it: who takes their gradient sets it."""
 
     def __init__(self, cfg: Config, tensors: dict, device="cuda"):
         self.cfg = cfg
@@ -464,21 +468,23 @@ class MoELayer:
         # the sync region (up to the logits) starts at zero; see moe_layer
         self.workspace[self.layout.sync:self.layout.logits].zero_()
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.tokens = None
 
     def __call__(self, x, out=None, stream=None):
         if out is None:
             out = _empty_like(x, stream)
         layer(self.cfg, x, self.weights, out, self.workspace, self.dev_status, stream)
+        self.tokens = x.shape[0]
         return out
 
     def experts_backward(self, dout, scratch, **kw):
         """Gradients of the routed experts of the last call, from its routing as the workspace
-        holds it (bf16 experts): the tokens (x, or xq and xq_scale) and the outputs as
-        ops.experts_backward takes them.  A shared expert's gradient is a call of its own
+        holds it (bf16 experts): dout for as many tokens as that call had, the tokens (x, or xq
+        and xq_scale) and the outputs as ops.experts_backward takes them.  A shared expert's gradient is a call of its own
         (E = 1, weights its gate), which dx_add joins to this one."""
         c, T, i32 = self.cfg, dout.shape[0], torch.int32
-        if T > c.T_max:
-            raise ValueError(f"dout: {T} tokens, the layer takes up to {c.T_max}")
+        if T != self.tokens:
+            raise ValueError(f"dout: {T} tokens, the layer's last call had {self.tokens}")
         w = self.tensors
         experts_backward(dout, self.view("offsets", i32, (c.E + 1,)),
                          self.view("row_to_flat", i32, (T * c.K,)),
@@ -525,9 +531,10 @@ class MoEBlock:
             add_rmsnorm(x, self.norm_weight, self.eps, y, residual=residual, h=h, yq=yq,
                         yq_scale=ys, stream=stream)
             layer_q8(L.cfg, y, yq, ys, L.weights, out, L.workspace, L.dev_status, stream)
+            L.tokens = T
         else:
             add_rmsnorm(x, self.norm_weight, self.eps, y, residual=residual, h=h, stream=stream)
-            layer(L.cfg, y, L.weights, out, L.workspace, L.dev_status, stream)
+            L(y, out, stream)
         return out, (x if h is None else h)
 
 
