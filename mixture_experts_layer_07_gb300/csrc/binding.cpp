@@ -2,8 +2,8 @@
 // in C because these calls are short -- a decode step's norm runs 1.7 us on the
 // GPU, and the same checks and the call through ctypes took the host 6.5 us.
 //
-// Every tensor is checked for its type, its number of values, contiguity and
-// that it is on a GPU, through the methods that torch.Tensor gives any caller (no torch headers, no
+// Every tensor is checked for its type, its number of values (the experts' matrices:
+// their shape), contiguity and that it is on a GPU, through the methods that torch.Tensor gives any caller (no torch headers, no
 // link against torch); the functions return the library's status.  The
 // library's entry points come by address from the ctypes binding, which owns
 // the library (connect).
@@ -58,6 +58,10 @@ struct Call {
   PyObject* const* a;
   bool bad = false;
   const char* host = nullptr;
+  PyObject* other = nullptr;  // what is said about a tensor of another shape
+  explicit Call(PyObject* const* args) : a(args) {}
+  Call(const Call&) = delete;
+  ~Call() { Py_XDECREF(other); }
 
   long long method_int(PyObject* t, PyObject* name) {
     PyObject* r = PyObject_CallMethodNoArgs(t, name);
@@ -184,6 +188,18 @@ struct Call {
     Py_XDECREF(s);
   }
 
+  // None, or a stack of matrices of these sizes: one with its matrices transposed holds as
+  // many values.  Told last, by `run`.
+  void check3(int i, int n, int rows, int cols, const char* name) {
+    if (bad || a[i] == Py_None) return;
+    int gn, gr, gc;
+    shape3(i, name, &gn, &gr, &gc);
+    if (bad || other || (gn == n && gr == rows && gc == cols)) return;
+    other = PyUnicode_FromFormat("%s: shape [%d, %d, %d] expected, got [%d, %d, %d]", name, n, rows,
+                                 cols, gn, gr, gc);
+    bad = !other;
+  }
+
   // a tensor of n values, bf16 or fp32, and its element type
   void* either(int i, long long n, int* dtype, const char* name) {
     if (bad || a[i] == Py_None) return nullptr;
@@ -227,7 +243,8 @@ PyObject* run(const Call& c, F&& f) {
     PyErr_Format(PyExc_ValueError, "%s: a tensor on the GPU expected", c.host);
     return nullptr;
   }
-  if (c.bad) return nullptr;
+  if (c.other && !c.bad) PyErr_SetObject(PyExc_ValueError, c.other);
+  if (c.other || c.bad) return nullptr;
   moe_status_t s;
   Py_BEGIN_ALLOW_THREADS
   s = f();
@@ -419,6 +436,12 @@ PyObject* experts_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c.shape2(0, "dout", &T, &H);
   c.shape2(4, "weights", &Tw, &K);
   c.shape3(5, "w1", &E, &I, &Hw);
+  c.check3(5, E, I, H, "w1");
+  c.check3(6, E, I, H, "w3");
+  c.check3(7, E, H, I, "w2");
+  c.check3(15, E, I, H, "dw1");
+  c.check3(16, E, I, H, "dw3");
+  c.check3(17, E, H, I, "dw2");
   const long long m = (long long)T * H, r = (long long)T * K, ew = (long long)E * I * H;
   const void* dout = c.ptr(0, BF16, m, "dout");
   const int32_t* off = c.ptr<int32_t>(1, I32, (long long)E + 1, "offsets");
