@@ -580,8 +580,18 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
         for (int s = 0; s < kStages; ++s)
           if (armed & (1u << s))
             if (!mbar_wait_bounded(full_bar(s), (armed_parity >> s) & 1u, nullptr, kWaitNs)) fail();
-      } else if (!ok) {
-        // given up: the copies count in the leader, so they get their time
+      }
+      // and the stages' last commits have arrived: they are sent to both CTAs, and one still on
+      // its way would find the shared memory of this SM's next CTA.  (The accumulators' are
+      // waited for by the epilogues, and the drain is the leader's alone.)
+      for (int s = 0; s < kStages && ok; ++s)
+        if (armed & (1u << s)) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(s), (armed_parity >> s) & 1u, abort_flag, kWaitNs));
+          if (!ok) fail();
+        }
+      if (rank == 1 && (!ok || *abort_flag)) {
+        // given up: the copies count in the leader and the commits are its own, so they get
+        // their time
         const uint64_t t0 = globaltimer_ns();
         for (int i = 0; i < (1 << 20) && globaltimer_ns() - t0 < 1000000; ++i) __nanosleep(1000);
       }
@@ -675,7 +685,7 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
       }
       if (issued) {
         // all MMAs of this warp complete before TMEM is released
-        if (elect_one()) tc_commit2(drain_bar);
+        if (elect_one()) tc_commit2(drain_bar, kLeader);
         if (!mbar_wait_bounded(drain_bar, 0, nullptr, kWaitNs)) fail();
       }
     }

@@ -331,12 +331,14 @@ MOE_DEVICE void tc_mma2_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uin
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// arrive on `bar` in both CTAs once every tcgen05 op issued so far by this thread completes
-MOE_DEVICE void tc_commit2(uint32_t bar) {
+// arrive on `bar` in both CTAs (or in those of the mask) once every tcgen05 op issued so far by
+// this thread completes.  A CTA has to wait for each arrival that is sent to it before it ends.
+constexpr uint16_t kLeader = 1;
+MOE_DEVICE void tc_commit2(uint32_t bar, uint16_t ctas = 3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
       "%1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(3))
+      "h"(ctas)
       : "memory");
 }
 
