@@ -854,7 +854,6 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
           // an expert without rows: zeros, or nothing to add
           if (a.accumulate) continue;
           for (int c = half * 128; c < c1; c += kCols) {
-            
             box_wait(lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i) box_piece(box, lane, i, make_uint4(0u, 0u, 0u, 0u));
@@ -870,7 +869,6 @@ products_kernel(const __grid_constant__ Maps maps, const GradArgs a) {
             uint32_t v[32];
             tc_ld_32x32b_x32(t0 - 128 * half + c, v);
             tc_wait_ld();
-            
             box_wait(lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i)

@@ -23,10 +23,6 @@ MOE_DEVICE void cp_async_4(uint32_t dst, const void* src, int src_bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
                : "memory");
 }
-// 8-byte cp.async
-MOE_DEVICE void cp_async_8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 MOE_DEVICE void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 MOE_DEVICE void cp_async_wait() {
@@ -112,15 +108,8 @@ MOE_DEVICE void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, 
 
 // Tile stores from shared memory (128-byte-swizzled as the loads land it); parts
 // of the box outside the tensor are left out.  A thread's stores form bulk groups:
-// commit, then wait until their shared memory is read, or until they are done.
-MOE_DEVICE void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(src), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-// the same for what is not read again soon: lines that L2 gives up first
+// commit, then wait until their shared memory is read, or until they are done.  `policy`
+// says how L2 treats the lines; l2_evict_first is for what is not read again soon.
 MOE_DEVICE uint64_t l2_evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -133,7 +122,7 @@ MOE_DEVICE void tma_store_3d_hint(const CUtensorMap* map, uint32_t src, int c0, 
       "r"(src), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
       : "memory");
 }
-// the same, adding to what the tensor holds (in the tensor's type)
+// a store that adds to what the tensor holds (in the tensor's type)
 MOE_DEVICE void tma_reduce_add_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
   asm volatile(
       "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::
