@@ -15,8 +15,11 @@ moe_add_rmsnorm_backward those of x and of the norm's weight.  Only the gate's
 two small products backwards are torch.  Gate, norm, experts (fp32 copies of
 their bf16 weights) and x learn.
 
-With q8 the two activations that are kept for the backward pass, h and y, are
-e4m3 codes (moe_pack_q8, and what the norm writes): half the memory.
+With q8 the backward pass reads the two activations that it needs, h and y, as
+e4m3 codes (moe_pack_q8, and what the norm writes): half the memory per layer in
+a model that keeps only those.  This one block has its bf16 buffers besides.
+The forward pass feeds the experts y in bf16, so the gradients are those at the
+values that the codes stand for.
 
     python examples/train_block.py [steps] [q8]
 """
@@ -103,8 +106,9 @@ class Block:
                            counts=self.counts, valid=self.valid, grad_losses=self.grad_losses,
                            dev_status=self.status)
         if self.q8:
-            ops.unpack_q8(self.yq, self.ys, self.y)  # y's memory was free in between
+            ops.unpack_q8(self.yq, self.ys, self.y)  # y's memory could have been another's in between
         d_gate = self.d_logits.t() @ self.y.float()
+        # the experts' part comes back rounded to bf16, and the sum is rounded once more
         dy = (self.d_logits @ self.wg + self.dy.float()).to(BF16)
         if self.q8:
             ops.add_rmsnorm_backward_q8(dy, self.hq, self.hs, self.rstd, self.norm, self.dx,

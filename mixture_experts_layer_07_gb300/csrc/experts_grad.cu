@@ -28,20 +28,28 @@
 //
 // Roundings: dg, du and w act to bf16 (the tensor cores' operands), the outputs once.
 // Everything else is fp32.  The tensor cores cut what falls off an fp32 sum, which
-// shortens it by about 10^-8 per K of 16; a, g and u, whose errors d_weights shows (its
+// shortens it by about 1.7e-8 per K of 16.  a, g and u, whose errors d_weights shows (its
 // fp32 is not behind a rounding to bf16), are therefore taken out of TMEM every 256 of K
-// (the first 512 of a long one) and added in registers: d_weights is 7e-7 to 9e-7 off 64
-// bits whatever H is, 9e-6 at H = 2880 in one go.  No atomics: sums have an order that the sizes and the routing fix.
+// (the first 512 of a long one) and added in registers: d_weights is at most 9.2e-7 off 64
+// bits whatever H is (H = 128 3.4e-7, 1024 6.6e-7, 1536 9.2e-7, 8192 7.2e-7), 9e-6 at
+// H = 2880 in one go.  The sums of the matrices' gradients (K = an expert's rows) and of dx
+// (K = 2 I) stay in TMEM: their operands' roundings to bf16 are far above what is cut there.
+// fp32 gradients of an expert with 8192 rows end 8.6e-6 too short, with 32768 rows 3.4e-5;
+// the operands' roundings put them 1.7e-3 off where the rows have no common direction, 3e-4
+// at 32768 rows that have one.  No atomics: sums have an order that the sizes and the
+// routing fix.
 //
 // Measured on one GB300 (copy rate 6797 GB/s, bf16 1947 TFLOP/s), per call in a graph of them:
-//   T = 4096, H = I = 2880, E = 32, K = 4, from codes  1830 us (2343 with single CTAs); the
-//     tensor cores' 1116 us, at the lower clock of long products, are the bound: part 0 is
+//   T = 4096, H = I = 2880, E = 32, K = 4, from codes  1840 us, 1750 to 1885 with the clock,
+//     which the power cap holds at 1560 to 1720 of 2070 MHz (2343 with single CTAs); the
+//     tensor cores' 1116 us at full clock are the bound: part 0 is
 //     held by its loads (83 bytes per clock and SM at full rate) and by what of its epilogue
 //     the next unit's first products do not hide, part 1 by loads and stores on the same path
-//   T = 2048, H = 2048, I = 768, E = 128, K = 8        711 us; memory: weights are read in
+//   T = 2048, H = 2048, I = 768, E = 128, K = 8        710 us; memory: weights are read in
 //     part 0 and, but for W2, again in part 1 (6.1 and 6.0 TB/s under the profiler)
-//   T = 64, H = 2048, I = 512, E = 512, K = 10         1081 us, floor 948: the matrices'
-//     gradients, mostly zeros or one row's, have to be written
+//   T = 64, H = 2048, I = 512, E = 512, K = 10         1082 us, floor 948: the matrices'
+//     gradients, mostly zeros or one row's, have to be written (fp32 1597 us, floor 1422;
+//     added to fp32 2025, floor 1622)
 //   T = 100, H = 256, I = 128, E = 8, K = 2            18 us: four dependent launches
 #include <cuda.h>
 
@@ -339,7 +347,11 @@ struct Walk {
       total = tokens = __ldg(&a.plan->tiles[0]) * wI;
     } else {
       most = kDxTokens;
-      // the gradient of x first: its units are the long ones
+      // The gradient of x first, whichever units are longer (2 I against the expert's rows): with
+      // the matrices first T = 4096, H = I = 2880 1890 -> 1925 us, small batches 4 to 7 % more,
+      // T = 64, E = 512 1102 -> 1081.  Units go to the pairs by a fixed stride, so shares are
+      // uneven where kinds differ: T = 4096, I = 512, one expert has 128 units of K = 1024 and 48
+      // of 4096 for 76 pairs, the longest share 6144 of K, the mean 4312.
       tokens = a.dx ? __ldg(&a.plan->tiles[1]) * wH : 0;
       total = tokens + (a.dw ? a.E * 3 * wI * wH : 0);
     }
